@@ -71,6 +71,15 @@ class NF4WeightC(ctypes.Structure):
                 ("dq_format", ctypes.c_int32)]
 
 
+class Act8C(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("m", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class AdapterSetC(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("count", ctypes.c_int32),
+                ("r", ctypes.c_int32)]
+
+
 _LIB = None
 
 _SIGNATURES = {
@@ -124,6 +133,22 @@ _SIGNATURES = {
                                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
                                                    ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
                                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_act_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_act_dequant": (ctypes.c_int, [ctypes.POINTER(Act8C), ctypes.c_void_p, ctypes.c_void_p]),
+    "qlora_linear_bwd_act8": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(Act8C), ctypes.c_void_p, ctypes.c_int64,
+                                             ctypes.POINTER(NF4WeightC), ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_linear_fwd_multi": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(NF4WeightC),
+                                              ctypes.POINTER(AdapterSetC), ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_linear_bwd_multi": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(Act8C), ctypes.c_void_p,
+                                              ctypes.c_int64, ctypes.POINTER(NF4WeightC), ctypes.POINTER(AdapterSetC),
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qlora_multi_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                      ctypes.c_int32, ctypes.c_int32]),
     "qlora_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p]),
     "qlora_selftest_div255": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
 }
@@ -445,6 +470,198 @@ def qlora_linear_fwd_noalloc(X: torch.Tensor, w: NF4Weight, A: Optional[torch.Te
            lib().qlora_linear_fwd_noalloc(X.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
                                           out.data_ptr(), _stream(stream)))
     return out
+
+
+@dataclass
+class Act8:
+    """An 8-bit activation checkpoint of a bf16 tensor [m x k]."""
+    codes: torch.Tensor          # int8 [m, k]
+    scale: torch.Tensor          # bfloat16 [m, k/64]
+    m: int
+    k: int
+
+    @classmethod
+    def empty(cls, m: int, k: int, device) -> "Act8":
+        return cls(torch.empty(m, k, dtype=torch.int8, device=device),
+                   torch.empty(m, k // BLOCK, dtype=torch.bfloat16, device=device), m, k)
+
+    def c_struct(self) -> Act8C:
+        return Act8C(self.codes.data_ptr(), self.scale.data_ptr(), self.m, self.k)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scale.numel()
+
+
+def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device) -> None:
+    """The tensor is a contiguous CUDA tensor of this type, shape and device."""
+    if t is None:
+        return
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _need_act8(act: Act8, m: int, k: int, device) -> None:
+    if act.m != m or act.k != k:
+        raise ValueError(f"the checkpoint holds [{act.m} x {act.k}], not [{m} x {k}]")
+    _need(act.codes, "codes", torch.int8, (m, k), device)
+    _need(act.scale, "scale", torch.bfloat16, (m, k // BLOCK), device)
+
+
+def _need_weight(w: NF4Weight, device) -> None:
+    if w.codes.device != device:
+        raise ValueError(f"the weight is on {w.codes.device}, not on {device}")
+
+
+def _need_ws(ws: Optional[torch.Tensor], device) -> None:
+    _need_cuda(ws)
+    if ws is not None and ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+
+
+def _stream_on(device: torch.device, stream) -> Optional[int]:
+    """The stream's handle; the default is the current stream of the tensors'
+    device, which must be the current device (the library launches there)."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def qlora_act_quantize(X: torch.Tensor, out: Optional[Act8] = None, stream=None) -> Act8:
+    """X bf16 [m x k] -> its 8-bit checkpoint: per 64 elements of a row
+    scale = bf16(max|x| / 127), codes = rint(x / scale)."""
+    if X.dim() != 2 or X.shape[1] % BLOCK:
+        raise ValueError("X must be a 2-D tensor with a row length that is a multiple of 64")
+    m, k = X.shape
+    _need(X, "X", torch.bfloat16, (m, k), None)
+    if out is None:
+        out = Act8.empty(m, k, X.device)
+    _need_act8(out, m, k, X.device)
+    _check("qlora_act_quantize", lib().qlora_act_quantize(X.data_ptr(), m, k, out.codes.data_ptr(),
+                                                          out.scale.data_ptr(), _stream_on(X.device, stream)))
+    return out
+
+
+def qlora_act_dequant(act: Act8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The checkpoint's X^ = bf16(codes . scale) [m x k]."""
+    dev = act.codes.device
+    _need_act8(act, act.m, act.k, dev)
+    if out is None:
+        out = torch.empty(act.m, act.k, dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (act.m, act.k), dev)
+    a = act.c_struct()
+    _check("qlora_act_dequant", lib().qlora_act_dequant(ctypes.byref(a), out.data_ptr(), _stream_on(dev, stream)))
+    return out
+
+
+def qlora_linear_bwd_act8(dY: torch.Tensor, act: Act8, w: NF4Weight, A: torch.Tensor, B: torch.Tensor, r: int,
+                          scale: float, T: torch.Tensor, dX: Optional[torch.Tensor] = None,
+                          dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None, want_dx: bool = True,
+                          ws: Optional[torch.Tensor] = None, stream=None):
+    """(dX or None, dA, dB) as qlora_linear_bwd with X read from its 8-bit
+    checkpoint; T = the forward's bf16(s X A^T) [m x r]."""
+    m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
+    if dX is None and want_dx:
+        dX = torch.empty(m, k, dtype=bf, device=dev)
+    if dA is None:
+        dA = torch.empty(r, k, dtype=bf, device=dev)
+    if dB is None:
+        dB = torch.empty(n, r, dtype=bf, device=dev)
+    for t, name, shape in ((dY, "dY", (m, n)), (A, "A", (r, k)), (B, "B", (n, r)), (T, "T", (m, r)),
+                           (dX, "dX", (m, k)), (dA, "dA", (r, k)), (dB, "dB", (n, r))):
+        _need(t, name, bf, shape, dev)
+    _need_act8(act, m, k, dev)
+    _need_weight(w, dev)
+    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, dev)
+    _need_ws(ws, dev)
+    w_c, a_c = w.c_struct(), act.c_struct()
+    _check("qlora_linear_bwd_act8",
+           lib().qlora_linear_bwd_act8(dY.data_ptr(), ctypes.byref(a_c), _ptr(T), m, ctypes.byref(w_c), A.data_ptr(),
+                                       B.data_ptr(), r, float(scale), _ptr(dX), dA.data_ptr(), dB.data_ptr(), _ptr(ws),
+                                       ws_bytes, _stream_on(dev, stream)))
+    return dX, dA, dB
+
+
+def qlora_multi_workspace_bytes(op: int, m: int, n: int, k: int, r: int, count: int) -> int:
+    return int(lib().qlora_multi_workspace_bytes(op, m, n, k, r, count))
+
+
+def _adapter_set(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor, m: int, w: NF4Weight, dev):
+    if A.dim() != 3:
+        raise ValueError("A must be a 3-D tensor [count x r x k]")
+    count, r = A.shape[0], A.shape[1]
+    _need(A, "A", torch.bfloat16, (count, r, w.k), dev)
+    _need(B, "B", torch.bfloat16, (count, w.n, r), dev)
+    _need(scale, "scale", torch.float32, (count,), dev)
+    _need(ids, "ids", torch.int32, (m,), dev)
+    _need_weight(w, dev)
+    return AdapterSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), count, r), count, r
+
+
+def _multi_workspace(op, m, n, k, r, count, ws, device):
+    if ws is None:
+        need = qlora_multi_workspace_bytes(op, m, n, k, r, count)
+        # Sizes the library refuses have no workspace; the call reports them.
+        ws = torch.empty(need if need < 1 << 62 else 0, dtype=torch.uint8, device=device)
+    _need_ws(ws, device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def qlora_linear_fwd_multi(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                           ids: torch.Tensor, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Y[i] = bf16(X[i] . W^T + bf16(s_a X[i] A_a^T) . B_a^T), a = ids[i]; an
+    id outside [0, count) means no adapter.  X bf16 [m x k], A [count x r x k],
+    B [count x n x r], scale fp32 [count], ids int32 [m].  The first m*r*2
+    bytes of `ws` hold T afterwards."""
+    m, dev = X.shape[0], X.device
+    if out is None:
+        out = torch.empty(m, w.n, dtype=torch.bfloat16, device=dev)
+    _need(X, "X", torch.bfloat16, (m, w.k), dev)
+    _need(out, "out", torch.bfloat16, (m, w.n), dev)
+    set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
+    ws, ws_bytes = _multi_workspace(QLORA_OP_FWD, m, w.n, w.k, r, count, ws, dev)
+    w_c = w.c_struct()
+    _check("qlora_linear_fwd_multi",
+           lib().qlora_linear_fwd_multi(X.data_ptr(), m, ctypes.byref(w_c), ctypes.byref(set_c), ids.data_ptr(),
+                                        out.data_ptr(), ws.data_ptr(), ws_bytes, _stream_on(dev, stream)))
+    return out
+
+
+def qlora_linear_bwd_multi(dY: torch.Tensor, X, w: NF4Weight, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                           ids: torch.Tensor, T: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None,
+                           dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None, want_dx: bool = True,
+                           ws: Optional[torch.Tensor] = None, stream=None):
+    """(dX or None, dA [count x r x k], dB [count x n x r]) of the layer whose
+    rows have their own adapters (see qlora_linear_fwd_multi).  X is the bf16
+    input or its Act8 checkpoint; T the forward's, required with a checkpoint."""
+    m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
+    set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
+    if dX is None and want_dx:
+        dX = torch.empty(m, k, dtype=bf, device=dev)
+    if dA is None:
+        dA = torch.empty(count, r, k, dtype=bf, device=dev)
+    if dB is None:
+        dB = torch.empty(count, n, r, dtype=bf, device=dev)
+    act = X if isinstance(X, Act8) else None
+    if act is not None:
+        _need_act8(act, m, k, dev)
+        X = None
+    for t, name, shape in ((dY, "dY", (m, n)), (X, "X", (m, k)), (T, "T", (m, r)), (dX, "dX", (m, k)),
+                           (dA, "dA", (count, r, k)), (dB, "dB", (count, n, r))):
+        _need(t, name, bf, shape, dev)
+    ws, ws_bytes = _multi_workspace(QLORA_OP_LORA_BWD, m, n, k, r, count, ws, dev)
+    w_c = w.c_struct()
+    a_c = ctypes.byref(act.c_struct()) if act is not None else None
+    _check("qlora_linear_bwd_multi",
+           lib().qlora_linear_bwd_multi(dY.data_ptr(), _ptr(X), a_c, _ptr(T), m, ctypes.byref(w_c),
+                                        ctypes.byref(set_c), ids.data_ptr(), _ptr(dX), dA.data_ptr(), dB.data_ptr(),
+                                        ws.data_ptr(), ws_bytes, _stream_on(dev, stream)))
+    return dX, dA, dB
 
 
 def qlora_selftest_bounded_wait(limit_ns: int, expired: Optional[torch.Tensor] = None, stream=None) -> None:

@@ -62,6 +62,28 @@ int check_adapter(const uint16_t *A, const uint16_t *B, int32_t r, bool *use) {
   return QLORA_OK;
 }
 
+// An adapter set and the ids of m rows.  A and B must hold count >= 1
+// adapters; scale and ids need only their own type's alignment.
+int check_adapters(const qlora_adapter_set *a, const int32_t *ids, int64_t m) {
+  if (!a || !a->A || !a->B || !a->scale) return QLORA_ERR_NULL;
+  if (a->r <= 0 || a->r > 256 || (a->r % 16) != 0) return QLORA_ERR_SHAPE;
+  if (a->count <= 0 || a->count > QLORA_MULTI_MAX_ADAPTERS) return QLORA_ERR_SHAPE;
+  if (m < 0 || m > QLORA_MULTI_MAX_ROWS) return QLORA_ERR_SHAPE;
+  if (!aligned16(a->A) || !aligned16(a->B)) return QLORA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(a->scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(ids) & 3u) != 0)
+    return QLORA_ERR_ALIGN;
+  if (m > 0 && !ids) return QLORA_ERR_NULL;
+  return QLORA_OK;
+}
+
+// A checkpoint of an [m x k] tensor.
+int check_act8(const qlora_act8 *x, int64_t m, int64_t k) {
+  if (!x || !x->codes || !x->scale) return QLORA_ERR_NULL;
+  if (x->m != m || x->k != k) return QLORA_ERR_SHAPE;
+  if (!aligned16(x->codes) || !aligned16(x->scale)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
 WeightView view(const qlora_nf4_weight *w) {
   return WeightView{w->codes, w->absmax_q, w->group_scale, w->n, w->k, &codebook_tables(w->codebook),
                     mean_ptr(w->group_scale, w->n * w->k / 64, w->dq_format)};
@@ -153,6 +175,27 @@ int validate_fwd(const uint16_t *X, int64_t m, const qlora_nf4_weight *w, const 
   return QLORA_OK;
 }
 
+namespace {
+
+// The weight-streaming forward (m <= 16): decode sizes take the per-warp
+// streaming kernel; the rest (m > 4, or K beyond one cluster's warps) the
+// CTA-ring kernel.
+cudaError_t launch_small_m(const uint16_t *X, int64_t m, const qlora_nf4_weight *w, const uint16_t *T,
+                           const uint16_t *B, int32_t r, uint16_t *Y, cudaStream_t s, bool pdl, const int32_t *ids,
+                           int32_t adapters) {
+  // One adapter for all keeps the plain levels, whose results callers have;
+  // many adapters take the ones that lose less to bf16.
+  const Nf4Tables &tab = ids ? stream_tables(w->codebook).tab : codebook_tables(w->codebook);
+  const float unscale = ids ? stream_tables(w->codebook).unscale : 1.0f;
+  return gemv_stream_supported(m, w->n, w->k)
+             ? launch_gemv_stream(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T, B, r, Y,
+                                  tab, s, pdl, ids, adapters, unscale)
+             : launch_gemv_fwd(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T, B, r, Y, tab,
+                               s, pdl, ids, adapters, unscale);
+}
+
+}  // namespace
+
 int launch_fwd(const uint16_t *X, const uint16_t *Xa, int64_t m, const qlora_nf4_weight *w, const uint16_t *A,
                const uint16_t *B, int32_t r, float scale, uint16_t *Y, uint16_t *T, cudaStream_t s) {
   const bool lora = T != nullptr;
@@ -163,15 +206,8 @@ int launch_fwd(const uint16_t *X, const uint16_t *Xa, int64_t m, const qlora_nf4
   if (m <= kSmallM) {
     if (lora) e = launch_lora_proj_small(Xa, m, w->k, A, r, scale, T, s);
     if (e == cudaSuccess) e = prof_mark(t_prof_start, s);
-    if (e == cudaSuccess) {
-      // Decode sizes take the per-warp streaming kernel; the rest (m > 4,
-      // or K beyond one cluster's warps) the CTA-ring kernel.
-      e = gemv_stream_supported(m, w->n, w->k)
-              ? launch_gemv_stream(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T,
-                                   lora ? B : nullptr, lora ? r : 0, Y, codebook_tables(w->codebook), s, pdl)
-              : launch_gemv_fwd(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T,
-                                lora ? B : nullptr, lora ? r : 0, Y, codebook_tables(w->codebook), s, pdl);
-    }
+    if (e == cudaSuccess)
+      e = launch_small_m(X, m, w, T, lora ? B : nullptr, lora ? r : 0, Y, s, pdl, nullptr, 0);
   } else {
     if (lora) e = tc_proj_kmajor(Xa, m, w->k, A, r, scale, T, s);
     if (e == cudaSuccess) e = prof_mark(t_prof_start, s);
@@ -180,6 +216,71 @@ int launch_fwd(const uint16_t *X, const uint16_t *Xa, int64_t m, const qlora_nf4
   if (e == cudaSuccess) e = prof_mark(t_prof_stop, s);
   return cuda_status(e);
 }
+
+namespace {
+
+// The whole backward of one adapter, X given as bf16 or as its checkpoint X8.
+int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, const uint16_t *T, int64_t m,
+               const qlora_nf4_weight *w, const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX,
+               uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  int st = check_weight(w);
+  if (st != QLORA_OK) return st;
+  if (!A || !B || !dA || !dB) return QLORA_ERR_NULL;
+  if (r <= 0 || r > 256 || (r % 16) != 0) return QLORA_ERR_SHAPE;
+  if (m < 0 || m > (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB)) return QLORA_ERR_ALIGN;
+  if ((dX && !aligned16(dX)) || (T && !aligned16(T))) return QLORA_ERR_ALIGN;
+  if (m > 0) {
+    if ((!X && !X8) || !dY) return QLORA_ERR_NULL;
+    if (!aligned16(X) || !aligned16(dY)) return QLORA_ERR_ALIGN;
+    if (X8) {
+      st = check_act8(X8, m, w->k);
+      if (st != QLORA_OK) return st;
+    }
+    const size_t need = qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, w->n, w->k, r);
+    if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  }
+  st = check_device();
+  if (st != QLORA_OK) return st;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t n = w->n, k = w->k;
+  if (m == 0) {
+    cudaError_t e = cudaMemsetAsync(dA, 0, static_cast<size_t>(r) * static_cast<size_t>(k) * 2u, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, static_cast<size_t>(n) * static_cast<size_t>(r) * 2u, s);
+    return cuda_status(e);
+  }
+  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
+  uint16_t *U = static_cast<uint16_t *>(ws);
+  uint16_t *Tw = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + mr);
+  void *scratch = static_cast<uint8_t *>(ws) + 2 * mr;
+  const size_t scratch_bytes = ws_bytes - 2 * mr;
+  // U once, for the input gradient and for dA; T from the forward when given.
+  // With r <= 64, U and dB come from one pass over dY.
+  const bool one_pass = plan_dy_pass(m, n, r).ok;
+  cudaError_t e = cudaSuccess;
+  if (T == nullptr) e = tc_proj_kmajor(X, m, k, A, r, scale, Tw, s);                   // T = bf16(s X A^T)
+  if (e == cudaSuccess)
+    e = one_pass ? launch_dy_pass(dY, m, n, B, T ? T : Tw, r, scale, U, dB, scratch, scratch_bytes, s,
+                                  t_prof_start == nullptr)                             // U and dB = dY^T T
+                 : tc_proj_mnmajor(dY, m, n, B, r, scale, U, s);                       // U = bf16(s dY B)
+  // The input-gradient kernel needs U only for its adapter k-steps: it is
+  // launched as a programmatic dependent of the kernel that writes U, which
+  // directly precedes it (unless the caller times the main kernel alone).
+  const bool pdl = t_prof_start == nullptr;
+  if (e == cudaSuccess) e = prof_mark(t_prof_start, s);
+  if (e == cudaSuccess && dX) e = tc_bwd_dx(dY, m, view(w), U, A, r, dX, s, pdl);      // dX = dY W^ + U A
+  if (e == cudaSuccess) e = prof_mark(t_prof_stop, s);
+  const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
+  if (e == cudaSuccess)
+    e = X8 ? launch_group_grads(nullptr, &x8, m, k, U, r, nullptr, dA, true, s)
+           : tc_tn_skinny(X, m, k, U, r, dA, true, s);                                    // dA = U^T X
+  if (e == cudaSuccess && !one_pass) e = tc_tn_skinny(dY, m, n, T ? T : Tw, r, dB, false, s);   // dB = dY^T T
+  return cuda_status(e);
+}
+
+}  // namespace
 
 }  // namespace qlora
 
@@ -378,54 +479,17 @@ int qlora_lora_bwd(const uint16_t *X, const uint16_t *dY, int64_t m, int64_t n, 
 int qlora_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t m, const qlora_nf4_weight *w,
                      const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX, uint16_t *dA,
                      uint16_t *dB, void *ws, size_t ws_bytes, qlora_stream_t stream) {
-  int st = check_weight(w);
-  if (st != QLORA_OK) return st;
-  if (!A || !B || !dA || !dB) return QLORA_ERR_NULL;
-  if (r <= 0 || r > 256 || (r % 16) != 0) return QLORA_ERR_SHAPE;
-  if (m < 0 || m > (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
-  if (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB)) return QLORA_ERR_ALIGN;
-  if ((dX && !aligned16(dX)) || (T && !aligned16(T))) return QLORA_ERR_ALIGN;
-  if (m > 0) {
-    if (!X || !dY) return QLORA_ERR_NULL;
-    if (!aligned16(X) || !aligned16(dY)) return QLORA_ERR_ALIGN;
-    const size_t need = qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, w->n, w->k, r);
-    if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
-    if (!aligned16(ws)) return QLORA_ERR_ALIGN;
-  }
-  st = check_device();
-  if (st != QLORA_OK) return st;
+  return linear_bwd(dY, X, nullptr, T, m, w, A, B, r, scale, dX, dA, dB, ws, ws_bytes, stream);
+}
 
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t n = w->n, k = w->k;
-  if (m == 0) {
-    cudaError_t e = cudaMemsetAsync(dA, 0, static_cast<size_t>(r) * static_cast<size_t>(k) * 2u, s);
-    if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, static_cast<size_t>(n) * static_cast<size_t>(r) * 2u, s);
-    return cuda_status(e);
-  }
-  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
-  uint16_t *U = static_cast<uint16_t *>(ws);
-  uint16_t *Tw = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + mr);
-  void *scratch = static_cast<uint8_t *>(ws) + 2 * mr;
-  const size_t scratch_bytes = ws_bytes - 2 * mr;
-  // U once, for the input gradient and for dA; T from the forward when given.
-  // With r <= 64, U and dB come from one pass over dY.
-  const bool one_pass = plan_dy_pass(m, n, r).ok;
-  cudaError_t e = cudaSuccess;
-  if (T == nullptr) e = tc_proj_kmajor(X, m, k, A, r, scale, Tw, s);                   // T = bf16(s X A^T)
-  if (e == cudaSuccess)
-    e = one_pass ? launch_dy_pass(dY, m, n, B, T ? T : Tw, r, scale, U, dB, scratch, scratch_bytes, s,
-                                  t_prof_start == nullptr)                             // U and dB = dY^T T
-                 : tc_proj_mnmajor(dY, m, n, B, r, scale, U, s);                       // U = bf16(s dY B)
-  // The input-gradient kernel needs U only for its adapter k-steps: it is
-  // launched as a programmatic dependent of the kernel that writes U, which
-  // directly precedes it (unless the caller times the main kernel alone).
-  const bool pdl = t_prof_start == nullptr;
-  if (e == cudaSuccess) e = prof_mark(t_prof_start, s);
-  if (e == cudaSuccess && dX) e = tc_bwd_dx(dY, m, view(w), U, A, r, dX, s, pdl);      // dX = dY W^ + U A
-  if (e == cudaSuccess) e = prof_mark(t_prof_stop, s);
-  if (e == cudaSuccess) e = tc_tn_skinny(X, m, k, U, r, dA, true, s);                  // dA = U^T X
-  if (e == cudaSuccess && !one_pass) e = tc_tn_skinny(dY, m, n, T ? T : Tw, r, dB, false, s);   // dB = dY^T T
-  return cuda_status(e);
+int qlora_linear_bwd_act8(const uint16_t *dY, const qlora_act8 *X8, const uint16_t *T, int64_t m,
+                          const qlora_nf4_weight *w, const uint16_t *A, const uint16_t *B, int32_t r, float scale,
+                          uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes,
+                          qlora_stream_t stream) {
+  // An empty batch reads neither the checkpoint nor T.
+  static const qlora_act8 none{};
+  if (m != 0 && (!X8 || !T)) return QLORA_ERR_NULL;
+  return linear_bwd(dY, nullptr, X8 ? X8 : &none, T, m, w, A, B, r, scale, dX, dA, dB, ws, ws_bytes, stream);
 }
 
 int qlora_lora_dropout(const uint16_t *X, int64_t m, int64_t k, float p, uint64_t seed, uint64_t offset,
@@ -490,6 +554,120 @@ int qlora_linear_bwd_dx_dropout(const uint16_t *dY, int64_t m, const qlora_nf4_w
   cudaError_t e = tc_proj_mnmajor(dY, m, w->n, B, r, scale, U, s);       // U = bf16(s dY B)
   if (e == cudaSuccess) e = tc_bwd_dx(dY, m, view(w), nullptr, nullptr, 0, dX, s, false);
   if (e == cudaSuccess) e = tc_dropout_add(U, m, r, A, w->k, d, dX, s);
+  return cuda_status(e);
+}
+
+int qlora_act_quantize(const uint16_t *X, int64_t m, int64_t k, int8_t *codes, uint16_t *scale,
+                       qlora_stream_t stream) {
+  if (m < 0 || k <= 0 || (k % 64) != 0 || m > (int64_t(1) << 31) || k > (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
+  if (m > (int64_t(1) << 40) / k) return QLORA_ERR_SHAPE;
+  if (m == 0) return QLORA_OK;
+  if (!X || !codes || !scale) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scale)) return QLORA_ERR_ALIGN;
+  int st = check_device();
+  if (st != QLORA_OK) return st;
+  return cuda_status(launch_act_quantize(X, m * k, codes, scale, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qlora_act_dequant(const qlora_act8 *x, uint16_t *X, qlora_stream_t stream) {
+  if (!x) return QLORA_ERR_NULL;
+  if (x->m < 0 || x->k <= 0 || (x->k % 64) != 0 || x->m > (int64_t(1) << 31) || x->k > (int64_t(1) << 31))
+    return QLORA_ERR_SHAPE;
+  if (x->m > (int64_t(1) << 40) / x->k) return QLORA_ERR_SHAPE;
+  if (x->m == 0) return QLORA_OK;
+  if (!x->codes || !x->scale || !X) return QLORA_ERR_NULL;
+  if (!aligned16(x->codes) || !aligned16(x->scale) || !aligned16(X)) return QLORA_ERR_ALIGN;
+  int st = check_device();
+  if (st != QLORA_OK) return st;
+  return cuda_status(launch_act_dequant(x->codes, x->scale, x->m * x->k, X, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t qlora_multi_workspace_bytes(int op, int64_t m, int64_t n, int64_t k, int32_t r, int32_t count) {
+  if (m < 0 || m > QLORA_MULTI_MAX_ROWS || n <= 0 || k <= 0 || r <= 0 || count <= 0 ||
+      count > QLORA_MULTI_MAX_ADAPTERS)
+    return SIZE_MAX;
+  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
+  const size_t tiles = m > 0 ? round_up(tile_lists_bytes(m, count)) : 0;
+  switch (op) {
+    case QLORA_OP_FWD: return mr + (m > kSmallM ? tiles : 0);
+    case QLORA_OP_LORA_BWD: return 2 * mr + tiles + round_up(m > 0 ? group_rows_bytes(m, count) : 0);
+    default: return SIZE_MAX;
+  }
+}
+
+int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight *w, const qlora_adapter_set *a,
+                           const int32_t *ids, uint16_t *Y, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  int st = check_weight(w);
+  if (st == QLORA_OK) st = check_adapters(a, ids, m);
+  if (st != QLORA_OK || m == 0) return st;
+  if (!X || !Y) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y)) return QLORA_ERR_ALIGN;
+  const size_t need = qlora_multi_workspace_bytes(QLORA_OP_FWD, m, w->n, w->k, a->r, a->count);
+  if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  st = check_device();
+  if (st != QLORA_OK) return st;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const AdapterView ad{a->A, a->B, a->scale, ids, a->count, a->r};
+  uint16_t *T = static_cast<uint16_t *>(ws);
+  cudaError_t e;
+  if (m <= kSmallM) {
+    e = launch_multi_proj_small(X, m, w->k, ad, T, s);
+    if (e == cudaSuccess) e = launch_small_m(X, m, w, T, a->B, a->r, Y, s, true, ids, a->count);
+  } else {
+    const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
+    const TileLists lists = carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count);
+    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, s);
+    if (e == cudaSuccess) e = tc_multi(X, m, view(w), false, T, ad, lists, Y, s);
+  }
+  return cuda_status(e);
+}
+
+int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, const uint16_t *T, int64_t m,
+                           const qlora_nf4_weight *w, const qlora_adapter_set *a, const int32_t *ids, uint16_t *dX,
+                           uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes, qlora_stream_t stream) {
+  int st = check_weight(w);
+  if (st == QLORA_OK) st = check_adapters(a, ids, m);
+  if (st != QLORA_OK) return st;
+  if (!dA || !dB) return QLORA_ERR_NULL;
+  if (!aligned16(dA) || !aligned16(dB) || (dX && !aligned16(dX)) || (T && !aligned16(T))) return QLORA_ERR_ALIGN;
+  const int64_t n = w->n, k = w->k;
+  if (m > 0) {
+    // X from exactly one of the two; a checkpoint needs the forward's T.
+    if (!dY || (!X && !X8) || (X && X8) || (X8 && !T)) return QLORA_ERR_NULL;
+    if (!aligned16(dY) || (X && !aligned16(X))) return QLORA_ERR_ALIGN;
+    if (X8) {
+      st = check_act8(X8, m, k);
+      if (st != QLORA_OK) return st;
+    }
+    const size_t need = qlora_multi_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, a->r, a->count);
+    if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  }
+  st = check_device();
+  if (st != QLORA_OK) return st;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (m == 0) {
+    const size_t set = static_cast<size_t>(a->count) * static_cast<size_t>(a->r) * 2u;
+    cudaError_t e = cudaMemsetAsync(dA, 0, set * static_cast<size_t>(k), s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, set * static_cast<size_t>(n), s);
+    return cuda_status(e);
+  }
+  const AdapterView ad{a->A, a->B, a->scale, ids, a->count, a->r};
+  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
+  uint8_t *p = static_cast<uint8_t *>(ws);
+  uint16_t *U = reinterpret_cast<uint16_t *>(p), *Tw = reinterpret_cast<uint16_t *>(p + mr);
+  const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count);
+  const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(static_cast<size_t>(lists.bytes)), m, a->count);
+  cudaError_t e = launch_group_rows(ids, m, rows, s);
+  if (e == cudaSuccess && !T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, s);   // T = s_a X A_a^T
+  if (e == cudaSuccess) e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, s);   // U = s_a dY B_a
+  if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);     // dX = dY W^ + U A_a
+  const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
+  if (e == cudaSuccess) e = launch_group_grads(X, X8 ? &x8 : nullptr, m, k, U, a->r, &rows, dA, true, s);
+  if (e == cudaSuccess) e = launch_group_grads(dY, nullptr, m, n, T ? T : Tw, a->r, &rows, dB, false, s);
   return cuda_status(e);
 }
 

@@ -57,6 +57,7 @@
 // device error word on expiry); no kernel traps.
 #include "common.cuh"
 #include "internal.h"
+#include "multi.cuh"
 #include "tcgen05.cuh"
 
 namespace qlora {
@@ -99,9 +100,12 @@ struct __align__(64) PairParams {
   int num_main, num_lora;
   int pdl;
   Nf4Tables tab;
+  MultiParams multi;     // many adapters only
 };
 
-template <bool BWD>
+// MULTI: the rows' adapters differ; the adapter k-steps follow the list of
+// the pair's 512-row tile, each unit's product masked to its adapter's rows.
+template <bool BWD, bool MULTI>
 __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t xfull[kStages], wfull[kStages], empty[kStages];
@@ -153,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
 
   if (warp == 0) {
     // ------------------------------------------------------------ activation producer
+    int issued = 0;
     if (lane == 0) {
-      int issued = 0;
       for (int it = 0; it < total; ++it) {
         const int s = it % kStages;
         const uint32_t use = static_cast<uint32_t>(it / kStages);
@@ -190,6 +194,55 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
         }
         ++issued;
       }
+    }
+    if constexpr (MULTI) {
+      // 64 / width units a step: this CTA's rows of T (or U) at the unit's
+      // rank columns, and its half of the adapter matrix.  The whole warp
+      // walks the list, lane 0 issues.
+      griddep_wait();
+      const MultiTile t = multi_tile(p.multi, m_pair);
+      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
+      const uint32_t w = static_cast<uint32_t>(p.multi.width);
+      const int units = t.adapters * per_adapter;
+      AdapterWindow win;
+      int ok = __shfl_sync(0xffffffffu, issued, 0) == total;
+      for (int u0 = 0, it = total; u0 < units && ok; u0 += per_step, ++it) {
+        const int s = it % kStages;
+        const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
+        const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
+        const uint32_t xbar = mapa_shared(smem_u32(&xfull[s]), 0);
+        const int nu = units - u0 < per_step ? units - u0 : per_step;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(it / kStages) & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
+          if (ok) {
+            if (leader) mbar_arrive_expect_tx(&xfull[s], static_cast<uint32_t>(nu) * w * 2u * (512u + 256u));
+            ++issued;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int u = 0; u < nu; ++u) {
+          const int a = win.at(t, (u0 + u) / per_adapter), c = ((u0 + u) % per_adapter) * p.multi.width;
+          if (lane == 0 && ok) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int y = (m0 + h * 128 < p.m) ? m0 + h * 128 : 0;
+              tma_load_2d_pair(xa + h * kASub + u * 256u * w, &p.tmA2, xbar, c, y);
+            }
+            if (!BWD) {
+              tma_load_3d_pair(wb + u * 256u * w, &p.tmB2, xbar, c, (c0 < p.n) ? static_cast<int>(c0) : 0, a);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int64_t col = c0 + 64 * j;
+                tma_load_3d_pair(wb + j * 8192u + u * 128u * w, &p.tmB2, xbar, col < p.k ? static_cast<int>(col) : 0, c,
+                                 a);
+              }
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) {
       // Let the last copies land before the CTA may exit (the leader's xfull
       // also counts the peer's boxes).
       if (leader)
@@ -223,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
+    int ok = 1;
     if (leader && lane == 0) {
-      bool ok = true;
       for (int it = 0; it < total && ok; ++it) {
         const int s = it % kStages;
         const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
@@ -245,6 +298,48 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
         }
         umma_commit_pair_both(&empty[s]);
       }
+    }
+    if constexpr (MULTI) {
+      if (leader) {
+        griddep_wait();
+        const MultiTile t = multi_tile(p.multi, m_pair);
+        const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
+        const uint32_t w = static_cast<uint32_t>(p.multi.width);
+        const int units = t.adapters * per_adapter;
+        MaskWindow<4> win;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int u0 = 0, it = total; u0 < units && ok; u0 += per_step, ++it) {
+          const int s = it % kStages;
+          const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
+          const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
+          const int nu = units - u0 < per_step ? units - u0 : per_step;
+          if (lane == 0)
+            ok = mbar_wait_cluster_bounded(&xfull[s], static_cast<uint32_t>(it / kStages) & 1u, p.err, kErrTimeoutFullA);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (lane == 0) tc_fence_after();
+          for (int u = 0; u < nu; ++u) {
+            win.load(t, (u0 + u) / per_adapter);
+            if (lane == 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                for (uint32_t kk = 0; kk < w / 16u; ++kk) {
+                  const uint64_t ad =
+                      smem_desc_unit(xa + h * kASub + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
+                  const uint64_t bd = BWD ? smem_desc(wb + u * 128u * w + kk * 2048u, 8192u, 1024u)
+                                          : smem_desc_unit(wb + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
+                  // Rows 128 h .. of the even CTA's 256, then of the odd CTA's.
+                  umma_f16_pair_masked(tmem + static_cast<uint32_t>(h * kBN), ad, bd, kIdesc, win.off[h],
+                                       win.off[2 + h]);
+                }
+              }
+            }
+          }
+          if (lane == 0) umma_commit_pair_both(&empty[s]);
+        }
+      }
+    }
+    if (leader && lane == 0) {
       if (ok) umma_commit_pair_both(&acc_full);
     }
   } else {
@@ -399,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
   }
 }
 
-template <bool BWD>
+template <bool BWD, bool MULTI = false>
 cudaError_t launch_pair(const PairParams &p, int64_t m, int64_t out_cols, cudaStream_t stream) {
   static std::atomic<bool> configured[kMaxDevicesPerProcess] = {};
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(fused_pair_kernel<BWD>), static_cast<int>(kSmemBytes),
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(fused_pair_kernel<BWD, MULTI>), static_cast<int>(kSmemBytes),
                                 configured);
   if (e != cudaSuccess) return e;
   const int64_t pairs_m = (m + 2 * kRowsCta - 1) / (2 * kRowsCta);
@@ -420,7 +515,7 @@ cudaError_t launch_pair(const PairParams &p, int64_t m, int64_t out_cols, cudaSt
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.pdl ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, fused_pair_kernel<BWD>, p);
+  e = cudaLaunchKernelEx(&cfg, fused_pair_kernel<BWD, MULTI>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -474,6 +569,26 @@ cudaError_t fused_bwd_dx_large(const uint16_t *dY, int64_t m, const WeightView &
   p.out_cols = w.k;
   p.num_main = static_cast<int>((w.n + kBK - 1) / kBK);
   return launch_pair<true>(p, m, w.k, stream);
+}
+
+cudaError_t fused_multi_large(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
+                              const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream) {
+  // The adapter steps are the list's, so the kernel sees none of its own.
+  PairParams p = common_params(w, m, 0, false, false, out);
+  const int64_t in = bwd ? w.n : w.k, cols = bwd ? w.k : w.n;
+  const uint32_t width = static_cast<uint32_t>(unit_width(ad.r));
+  if (!encode_bf16_map(&p.tmA, L, m, in, 64, 128)) return cudaErrorInvalidValue;
+  if (!encode_codes_map(&p.tmCodes, w.codes, w.n, w.k / 2, 32, bwd ? 64 : kHalfN, false)) return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, width, 128)) return cudaErrorInvalidValue;
+  if (bwd ? !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)
+          : !encode_bf16_stack_map(&p.tmB2, ad.B, ad.count, w.n, ad.r, width, kHalfN))
+    return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p.tmOut, out, m, cols, 64, 256)) return cudaErrorInvalidValue;
+  p.out_cols = cols;
+  p.num_main = static_cast<int>((in + kBK - 1) / kBK);
+  p.pdl = 1;
+  p.multi = multi_params(ad, lists);
+  return bwd ? launch_pair<true, true>(p, m, cols, stream) : launch_pair<false, true>(p, m, cols, stream);
 }
 
 }  // namespace qlora

@@ -58,6 +58,9 @@ struct __align__(64) GemvParams {
   uint16_t *Y;
   unsigned *err;
   int64_t n, k;
+  const int32_t *ids;           // adapter of each token (null: one adapter for all)
+  int adapters;                 // B is [adapters x n x r]
+  float unscale;                // takes the levels' common factor out of the block constants
   int m, r;
   uint32_t x_box_bytes;         // bytes of one X box (64 columns x 8 or 16 token rows)
   Nf4Tables tab;
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_fwd_kernel(const __grid_cons
     // t (the group constant, fp32(S / 255) for linear 8-bit codes) of each
     // row's current group and the block where the next group starts.
     const bool fp8 = p.mu != nullptr;
-    const float mu = load_mu(p.mu);
+    const float mu = load_mu(p.mu) * p.unscale;
     float t0 = 0.f, t1 = 0.f;
     int next0 = kb_lo, next1 = kb_lo;
 
@@ -284,11 +287,11 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_fwd_kernel(const __grid_cons
       // Group constants: with 4-aligned blocks a group boundary falls on a
       // stage start; otherwise the slow path below takes it block by block.
       if (kb_st >= next0) {
-        t0 = group_constant(__ldg(p.group_scale + ((b0 + kb_st) >> 8)), fp8);
+        t0 = group_constant(__ldg(p.group_scale + ((b0 + kb_st) >> 8)), fp8) * p.unscale;
         next0 = kb_st + 256 - static_cast<int>((b0 + kb_st) & 255);
       }
       if (kb_st >= next1) {
-        t1 = group_constant(__ldg(p.group_scale + ((b1 + kb_st) >> 8)), fp8);
+        t1 = group_constant(__ldg(p.group_scale + ((b1 + kb_st) >> 8)), fp8) * p.unscale;
         next1 = kb_st + 256 - static_cast<int>((b1 + kb_st) & 255);
       }
       // A wait that gives up (it never should) ends the warp's loop on every
@@ -317,11 +320,11 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_fwd_kernel(const __grid_cons
         if (!fast) {
           const int kb = kb_st + b;
           if (kb == next0 && kb < kblocks) {
-            t0 = group_constant(__ldg(p.group_scale + ((b0 + kb) >> 8)), fp8);
+            t0 = group_constant(__ldg(p.group_scale + ((b0 + kb) >> 8)), fp8) * p.unscale;
             next0 += 256;
           }
           if (kb == next1 && kb < kblocks) {
-            t1 = group_constant(__ldg(p.group_scale + ((b1 + kb) >> 8)), fp8);
+            t1 = group_constant(__ldg(p.group_scale + ((b1 + kb) >> 8)), fp8) * p.unscale;
             next1 += 256;
           }
         }
@@ -379,9 +382,11 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_fwd_kernel(const __grid_cons
 #pragma unroll
     for (uint32_t peer = 0; peer < 8; ++peer)
       if (peer < csize) sum += part[peer];
-    if (p.r > 0) {
+    // The token's adapter; an id outside the set means none.
+    const int ad = p.ids ? __ldg(p.ids + mi) : 0;
+    if (p.r > 0 && (!p.ids || (ad >= 0 && ad < p.adapters))) {
       const uint16_t *trow = p.T + static_cast<int64_t>(mi) * p.r;
-      const uint16_t *brow = p.B + n * p.r;
+      const uint16_t *brow = p.B + (ad * p.n + n) * p.r;
       for (int j = 0; j < p.r; j += 8) {
         const uint4 tv = *reinterpret_cast<const uint4 *>(trow + j);
         const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(brow + j));
@@ -464,7 +469,8 @@ cudaError_t launch_lora_proj_small(const uint16_t *X, int64_t m, int64_t k, cons
 cudaError_t launch_gemv_fwd(const uint16_t *X, int64_t m, const uint8_t *codes, const uint8_t *absmax_q,
                             const float *group_scale, const float *mu, int64_t n, int64_t k, const uint16_t *T,
                             const uint16_t *B, int32_t r, uint16_t *Y, const Nf4Tables &tab,
-                            cudaStream_t stream, bool pdl) {
+                            cudaStream_t stream, bool pdl, const int32_t *ids, int32_t adapters,
+                            float unscale) {
   if (m <= 0) return cudaSuccess;
   GemvParams p{};
   if (!encode_codes_map(&p.tmCodes, codes, n, k / 2, 128, kRows, true)) return cudaErrorInvalidValue;
@@ -479,6 +485,9 @@ cudaError_t launch_gemv_fwd(const uint16_t *X, int64_t m, const uint8_t *codes, 
   p.mu = mu;
   p.T = T;
   p.B = B;
+  p.ids = ids;
+  p.adapters = adapters;
+  p.unscale = unscale;
   p.Y = Y;
   p.err = device_error_word();
   p.n = n;

@@ -79,10 +79,13 @@ struct __align__(64) StreamParams {
   const float *mu;               // E4M3 + mean format: the tensor mean; else null
   const uint16_t *X;             // [m x k] bf16
   const uint16_t *T;             // [m x r] bf16 (adapter intermediate) or null
-  const uint16_t *B;             // [n x r] bf16
+  const uint16_t *B;             // [n x r] bf16, or [adapters x n x r]
+  const int32_t *ids;            // adapter of each token (null: one adapter for all)
   uint16_t *Y;                   // [m x n] bf16
   unsigned *err;
   int64_t n, k;
+  int adapters;
+  float unscale;                 // takes the levels' common factor out of the block constants
   int m, r;
   int ntiles;                    // ceil(n / tile rows)
   int chunks;                    // ceil((k / 64) / 4)
@@ -254,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
                             : 0.f;
   build_pair_lut(dsmem, p.tab, threadIdx.x, kThreads);
   for (int i = threadIdx.x; i < nt * kTileRows * kMaxM; i += kThreads) red[i] = 0.f;
-  const auto gconst = [](float stored) { return FP8 ? stored : div255_rn(stored); };
+  const auto gconst = [&](float stored) { return (FP8 ? stored : div255_rn(stored)) * p.unscale; };
   if (static_cast<int>(threadIdx.x) < ngroups) ttab[threadIdx.x] = gconst(s_first);
   for (int i = threadIdx.x + kThreads; i < ngroups; i += kThreads)
     ttab[i] = gconst(__ldg(p.group_scale + min(gbase + i, glast)));
-  const float mu = FP8 ? __ldg(p.mu) : 0.f;
+  const float mu = FP8 ? __ldg(p.mu) * p.unscale : 0.f;
   __syncthreads();
 
   if (active) {
@@ -436,9 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
 #pragma unroll
     for (uint32_t peer = 0; peer < kMaxCluster; ++peer)
       if (peer < csize) sum += part[peer];
-    if (p.r > 0) {
+    // The token's adapter; an id outside the set means none.
+    const int ad = p.ids ? __ldg(p.ids + mi) : 0;
+    if (p.r > 0 && (!p.ids || (ad >= 0 && ad < p.adapters))) {
       const uint16_t *trow = p.T + static_cast<int64_t>(mi) * p.r;
-      const uint16_t *brow = p.B + n * p.r;
+      const uint16_t *brow = p.B + (ad * p.n + n) * p.r;
       for (int jr = 0; jr < p.r; jr += 8) {
         const uint4 tv = *reinterpret_cast<const uint4 *>(trow + jr);
         const uint4 bv = __ldg(reinterpret_cast<const uint4 *>(brow + jr));
@@ -513,7 +518,8 @@ bool gemv_stream_supported(int64_t m, int64_t n, int64_t k) {
 cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *codes, const uint8_t *absmax_q,
                                const float *group_scale, const float *mu, int64_t n, int64_t k, const uint16_t *T,
                                const uint16_t *B, int32_t r, uint16_t *Y, const Nf4Tables &tab,
-                               cudaStream_t stream, bool pdl) {
+                               cudaStream_t stream, bool pdl, const int32_t *ids, int32_t adapters,
+                               float unscale) {
   if (m <= 0) return cudaSuccess;
   if (!gemv_stream_supported(m, n, k)) return cudaErrorInvalidValue;
   const int64_t kblocks = k / 64;
@@ -527,6 +533,9 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
   p.X = X;
   p.T = T;
   p.B = B;
+  p.ids = ids;
+  p.adapters = adapters;
+  p.unscale = unscale;
   p.Y = Y;
   p.err = device_error_word();
   p.n = n;

@@ -21,6 +21,16 @@ const Nf4Tables &codebook_tables(int codebook);
 const QuantBuckets &codebook_buckets(int codebook);
 const Nf4Tables &nf4_tables();
 
+// A codebook's levels times a factor g that brings them close to bf16 numbers,
+// and 1 / g for the block constants.  The weight-streaming kernels multiply
+// bf16 levels and scale afterwards: with these tables the levels' rounding
+// costs 0.08 % (rms, NF4) instead of 0.14 %, and nothing for FP4 and INT4.
+struct StreamTables {
+  Nf4Tables tab;
+  float unscale;
+};
+const StreamTables &stream_tables(int codebook);
+
 // Device error word (bounded waits that gave up); one per device.
 unsigned *device_error_word();
 
@@ -67,10 +77,15 @@ struct DropoutParams {
 cudaError_t launch_dropout_apply(const uint16_t *X, int64_t numel, const DropoutParams &d, uint16_t *Xd,
                                  cudaStream_t stream);
 
-// TMA tensor maps (2D, row-major).  bf16: 128-byte swizzle.  codes: uint8
+// TMA tensor maps (2D, row-major).  bf16: the swizzle as wide as a box row
+// (128, 64 or 32 bytes).  codes: uint8
 // rows of packed codes, optional 128-byte swizzle.  False if encoding failed.
 bool encode_bf16_map(CUtensorMap *m, const uint16_t *ptr, int64_t rows, int64_t cols, uint32_t box_cols,
                      uint32_t box_rows);
+// 3D map over `count` row-major bf16 [rows x cols] matrices; boxes of
+// {box_cols, box_rows, 1} under the swizzle as wide as a box row.
+bool encode_bf16_stack_map(CUtensorMap *m, const uint16_t *ptr, int64_t count, int64_t rows, int64_t cols,
+                           uint32_t box_cols, uint32_t box_rows);
 // 3D map over `slabs` row-major fp32 [rows x cols] matrices; 128-byte
 // swizzled boxes of {box_cols (<= 32), box_rows, 1}.  Stores clip at the
 // slab's rows and columns.
@@ -106,11 +121,14 @@ cudaError_t launch_lora_proj_small(const uint16_t *X, int64_t m, int64_t k, cons
                                    int32_t r, float scale, uint16_t *T, cudaStream_t stream);
 
 // Y[m x n] = bf16(X . W^T + T . B^T) for m <= 16 (CTA-ring weight-streaming
-// kernel); with pdl it overlaps the preceding T projection.
+// kernel); with pdl it overlaps the preceding T projection.  With ids, B is
+// [adapters x n x r] and token i's adapter is ids[i] (none outside the set).
+// The levels of `tab` may carry a factor 1 / unscale (StreamTables).
 cudaError_t launch_gemv_fwd(const uint16_t *X, int64_t m, const uint8_t *codes,
                             const uint8_t *absmax_q, const float *group_scale, const float *mu, int64_t n,
                             int64_t k, const uint16_t *T, const uint16_t *B, int32_t r, uint16_t *Y,
-                            const Nf4Tables &tab, cudaStream_t stream, bool pdl);
+                            const Nf4Tables &tab, cudaStream_t stream, bool pdl, const int32_t *ids = nullptr,
+                            int32_t adapters = 0, float unscale = 1.0f);
 
 // Decode-sized forward (m <= 4, k/64 <= 512): per-warp TMA streams of the
 // codes, K split over a cluster.  Same contract as launch_gemv_fwd.
@@ -118,7 +136,8 @@ bool gemv_stream_supported(int64_t m, int64_t n, int64_t k);
 cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *codes,
                                const uint8_t *absmax_q, const float *group_scale, const float *mu,
                                int64_t n, int64_t k, const uint16_t *T, const uint16_t *B, int32_t r, uint16_t *Y,
-                               const Nf4Tables &tab, cudaStream_t stream, bool pdl);
+                               const Nf4Tables &tab, cudaStream_t stream, bool pdl, const int32_t *ids = nullptr,
+                            int32_t adapters = 0, float unscale = 1.0f);
 
 // tcgen05 paths -------------------------------------------------------------
 
@@ -188,5 +207,76 @@ cudaError_t tc_proj_mnmajor(const uint16_t *L, int64_t m, int64_t kc, const uint
 // or as [r x p] (transposed == true).
 cudaError_t tc_tn_skinny(const uint16_t *Lt, int64_t mc, int64_t p, const uint16_t *R, int32_t r,
                          uint16_t *out, bool transposed, cudaStream_t stream);
+
+// Cluster size that splits `ksteps` k-steps of a product with `tiles` output
+// tiles (tc_gemm.cu).
+int choose_split(int64_t tiles, int ksteps, int per_sm = 2);
+
+// Many adapters on one weight -------------------------------------------------
+
+// The adapters of a call (device pointers): A [count x r x k], B [count x n x r],
+// scale [count], and the adapter of each row (none outside [0, count)).
+struct AdapterView {
+  const uint16_t *A, *B;
+  const float *scale;
+  const int32_t *ids;
+  int32_t count, r;
+};
+
+// Per row tile (128 rows when m <= 128, else 512) of a batch, in int32 words:
+// [0] the number of adapters in the tile, [4 ..] their ids in order of first
+// appearance (`slots` entries), then per adapter rows/32 mask words whose bit
+// i is set for a row 32 w + i of that adapter.
+struct TileLists {
+  int32_t *base;
+  int64_t stride, tiles, bytes;
+  int32_t slots, rows;
+};
+TileLists carve_tile_lists(void *scratch, int64_t m, int32_t count);
+size_t tile_lists_bytes(int64_t m, int32_t count);
+
+// out[m x r] = bf16(s_a . L . A_a^T) (L = X [m x k]) or, through_b,
+// bf16(s_a . L . B_a) (L = dY [m x n]); zeros in rows without an adapter.
+// Fills `lists` too unless null.  m > 0.
+cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
+                              uint16_t *out, const TileLists *lists, cudaStream_t stream);
+// The first form for m <= 16 (no lists).
+cudaError_t launch_multi_proj_small(const uint16_t *X, int64_t m, int64_t k, const AdapterView &s, uint16_t *T,
+                                    cudaStream_t stream);
+
+// out = bf16(L . W^T + V . B_a^T) (forward: V = T) or bf16(L . W^ + V . A_a)
+// (bwd: V = U), launched as a programmatic dependent of the projection that
+// wrote V and `lists`.
+cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
+                     const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream);
+cudaError_t fused_multi_large(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
+                              const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream);
+
+// Each adapter's rows in ascending order: list[start[a] .. + count[a]), start
+// a multiple of 64, padded to whole 64s with the adapter's last row.
+struct GroupRows {
+  int32_t *start, *count, *list;
+  int32_t groups;
+};
+GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups);
+size_t group_rows_bytes(int64_t m, int32_t groups);
+cudaError_t launch_group_rows(const int32_t *ids, int64_t m, const GroupRows &g, cudaStream_t stream);
+
+// An 8-bit activation checkpoint: int8 codes [m x k], bf16 scales [m x k/64].
+struct Act8View {
+  const int8_t *codes;
+  const uint16_t *scale;
+};
+
+// out_g = sum over group g's rows i of L[i, :]^T . R[i, :]  [P x r], or
+// transposed [r x P]; L bf16 [m x P], or its checkpoint L8 (transposed output
+// only); one group of all rows when g is null.  Every group is written.
+cudaError_t launch_group_grads(const uint16_t *L, const Act8View *L8, int64_t m, int64_t P, const uint16_t *R,
+                               int32_t r, const GroupRows *g, uint16_t *out, bool transposed, cudaStream_t stream);
+
+// 8-bit activation checkpoints (act8.cu); numel % 64 == 0.
+cudaError_t launch_act_quantize(const uint16_t *X, int64_t numel, int8_t *codes, uint16_t *scale, cudaStream_t stream);
+cudaError_t launch_act_dequant(const int8_t *codes, const uint16_t *scale, int64_t numel, uint16_t *X,
+                               cudaStream_t stream);
 
 }  // namespace qlora

@@ -143,6 +143,49 @@ const QuantBuckets &codebook_buckets(int codebook) {
   return b[(codebook >= 0 && codebook < kCodebookCount) ? codebook : kCodebookNF4];
 }
 
+namespace {
+
+float bf16_rne(float x) {
+  uint32_t u;
+  std::memcpy(&u, &x, 4);
+  u = (u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u;
+  std::memcpy(&x, &u, 4);
+  return x;
+}
+
+// The factor g in {1 + i / 4096} whose multiples g . L lie closest to bf16
+// numbers (sum over the levels of (bf16(g L) / g - L)^2; the first minimum).
+StreamTables build_stream(const Nf4Tables &t) {
+  double best = std::numeric_limits<double>::infinity();
+  float g = 1.0f;
+  for (int i = 0; i < 4096; ++i) {
+    const float c = 1.0f + static_cast<float>(i) / 4096.0f;
+    double sum = 0.0;
+    for (int j = 0; j < 16; ++j) {
+      const double e = static_cast<double>(bf16_rne(t.level[j] * c)) / c - t.level[j];
+      sum += e * e;
+    }
+    if (sum < best) {
+      best = sum;
+      g = c;
+    }
+  }
+  StreamTables s{};
+  s.tab = t;
+  for (int j = 0; j < 16; ++j) s.tab.level[j] = t.level[j] * g;
+  s.unscale = 1.0f / g;
+  return s;
+}
+
+}  // namespace
+
+const StreamTables &stream_tables(int codebook) {
+  static const StreamTables s[kCodebookCount] = {build_stream(codebook_tables(kCodebookNF4)),
+                                                 build_stream(codebook_tables(kCodebookFP4)),
+                                                 build_stream(codebook_tables(kCodebookINT4))};
+  return s[(codebook >= 0 && codebook < kCodebookCount) ? codebook : kCodebookNF4];
+}
+
 const Nf4Tables &nf4_tables() { return codebook_tables(kCodebookNF4); }
 
 }  // namespace qlora

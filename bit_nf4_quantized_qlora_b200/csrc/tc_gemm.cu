@@ -39,24 +39,13 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "multi.cuh"
 #include "philox.cuh"
+#include "split_reduce.cuh"
 #include "tcgen05.cuh"
 
 namespace qlora {
 namespace {
-
-// 16 bytes (four fp32) at the same offset in CTA `rank`'s shared memory;
-// local_addr must be 16-byte aligned.
-__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t local_addr, uint32_t rank) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(remote)
-               : "memory");
-  return v;
-}
 
 constexpr int kBK = 64;                       // k-step: 64 bf16 = one swizzle row
 constexpr uint32_t kASub = 128u * kBK * 2u;   // 16 KB: one 128-row A tile
@@ -80,6 +69,7 @@ struct __align__(64) TcParams {
   float alpha;
   Nf4Tables tab;
   DropoutParams drop;   // masked-add epilogue only
+  MultiParams multi;    // many adapters only
 };
 
 // Epilogues: store bf16(alpha . acc), or (dropout) add the masked product to
@@ -89,8 +79,10 @@ enum : int { kEpiStore = 0, kEpiDropoutAdd = 1 };
 // ---- compile-time configuration -------------------------------------------
 
 template <int BN_, int MSUB_, bool A_MN_, bool B_NF4_, bool B_MN_, bool OUT_T_, bool SPLIT_ = false,
-          int EPI_ = kEpiStore>
+          int EPI_ = kEpiStore, bool MULTI_ = false>
 struct Cfg {
+  // The rows' adapters differ: the adapter k-steps follow the tile's list.
+  static constexpr bool MULTI = MULTI_;
   static constexpr int EPI = EPI_;
   static constexpr bool SPLIT = SPLIT_;   // contraction split over a cluster, DSMEM reduction
   static constexpr int BN = BN_;
@@ -132,6 +124,7 @@ struct Cfg {
   // output, column-major (128 fp32 per column) for a transposed one.
   static constexpr uint32_t PART_LD = static_cast<uint32_t>(BN) + 4u;
   static_assert(!SPLIT || STAGE_BYTES * STAGES >= 128u * PART_LD * 4u, "room for the fp32 partial tile");
+  static_assert(!MULTI || (B_NF4 && MSUB == 1), "many adapters: the NF4 products on 128-row tiles");
   static_assert(EPI == kEpiStore || (!SPLIT && !OUT_T && !B_NF4), "masked add: plain row-major output");
 };
 
@@ -187,8 +180,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    int issued = 0;
     if (lane == 0) {
-      int issued = 0;
       for (int it = it_begin; it < total; ++it) {
         const int li = it - it_begin;
         const int s = li % C::STAGES;
@@ -243,6 +236,49 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
         }
         ++issued;
       }
+    }
+    if constexpr (C::MULTI) {
+      // Adapter k-steps: this CTA's share of the tile's units, 64 rank columns
+      // a step; their operands come from the preceding projection.  The whole
+      // warp walks the list, lane 0 issues.
+      griddep_wait();
+      const MultiTile t = multi_tile(p.multi, 0);
+      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
+      const uint32_t w = static_cast<uint32_t>(p.multi.width);
+      const int units = t.adapters * per_adapter;
+      int lo, hi;
+      multi_share(units, per_step, &lo, &hi);
+      AdapterWindow win;
+      int ok = __shfl_sync(0xffffffffu, issued, 0) == n_iters;
+      for (int st = lo; st < hi && ok; ++st) {
+        const int li = n_iters + st - lo, s = li % C::STAGES;
+        const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
+        const int u0 = st * per_step, nu = units - u0 < per_step ? units - u0 : per_step;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u, p.err,
+                                 kErrTimeoutEmpty);
+          if (ok) {
+            mbar_arrive_expect_tx(&full_a[s], static_cast<uint32_t>(nu) * w * (256u + 2u * C::BN));
+            ++issued;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (int u = 0; u < nu; ++u) {
+          const int a = win.at(t, (u0 + u) / per_adapter), c = ((u0 + u) % per_adapter) * p.multi.width;
+          if (lane == 0 && ok) {
+            tma_load_2d(a_s + u * 256u * w, &p.tmA2, &full_a[s], c, m_tile * C::BM);
+            if (!C::B_MN) {
+              tma_load_3d(b_s + u * 2u * C::BN * w, &p.tmB2, &full_a[s], c, n_tile * C::BN, a);
+            } else {
+#pragma unroll
+              for (int j = 0; j < C::BN / 64; ++j)
+                tma_load_3d(b_s + j * 8192u + u * 128u * w, &p.tmB2, &full_a[s], n_tile * C::BN + 64 * j, c, a);
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) {
       // Drain: every issued copy has landed before the CTA may exit.
       for (int it = issued - C::STAGES < 0 ? 0 : issued - C::STAGES; it < issued; ++it)
         mbar_wait_bounded(&full_a[it % C::STAGES], static_cast<uint32_t>(it / C::STAGES) & 1u, p.err,
@@ -250,8 +286,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    int ok = 1;
     if (lane == 0) {
-      bool ok = true;
       for (int it = it_begin; it < total && ok; ++it) {
         const int li = it - it_begin;
         const int s = li % C::STAGES;
@@ -275,6 +311,42 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
         }
         umma_commit(&empty_bar[s]);
       }
+    }
+    if constexpr (C::MULTI) {
+      griddep_wait();
+      const MultiTile t = multi_tile(p.multi, 0);
+      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
+      const uint32_t w = static_cast<uint32_t>(p.multi.width);
+      const int units = t.adapters * per_adapter;
+      int lo, hi;
+      multi_share(units, per_step, &lo, &hi);
+      MaskWindow<1> win;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int st = lo; st < hi && ok; ++st) {
+        const int li = n_iters + st - lo, s = li % C::STAGES;
+        const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
+        const int u0 = st * per_step, nu = units - u0 < per_step ? units - u0 : per_step;
+        if (lane == 0)
+          ok = mbar_wait_bounded(&full_a[s], static_cast<uint32_t>(li / C::STAGES) & 1u, p.err, kErrTimeoutFullA);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane == 0) tc_fence_after();
+        for (int u = 0; u < nu; ++u) {
+          win.load(t, (u0 + u) / per_adapter);
+          if (lane == 0) {
+            for (uint32_t kk = 0; kk < w / 16u; ++kk) {
+              const uint64_t ad = smem_desc_unit(a_s + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
+              const uint64_t bd = C::B_MN
+                                      ? smem_desc(b_s + u * 128u * w + kk * 2048u, 8192u, 1024u)
+                                      : smem_desc_unit(b_s + u * 2u * C::BN * w + kk * 32u, 16u, 16u * w, p.multi.width);
+              umma_f16_masked(tmem, ad, bd, C::IDESC, win.off[0]);
+            }
+          }
+        }
+        if (lane == 0) umma_commit(&empty_bar[s]);
+      }
+    }
+    if (lane == 0) {
       if (ok) umma_commit(&acc_bar);
     }
   } else {
@@ -487,94 +559,11 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
   tc_fence_before();
   __syncthreads();
   if (C::SPLIT) {
-    // Reduce the cluster's partial tiles through distributed shared memory:
-    // CTA `rank` finishes a share of the tile's rows that exist in the output
-    // (in whole groups of four rows for a transposed output).
+    // The cluster's partial tiles, through distributed shared memory.
     cluster_sync_all();
-    const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int64_t left = static_cast<int64_t>(p.out_rows) - static_cast<int64_t>(m_tile) * C::BM;
-    const uint32_t valid = static_cast<uint32_t>(left < 128 ? (left > 0 ? left : 0) : 128);
-    const uint32_t units = C::OUT_T ? (valid + 3u) / 4u : valid;
-    const int u_lo = static_cast<int>((units * rank) / size), u_hi = static_cast<int>((units * (rank + 1)) / size);
-    const int nu = u_hi - u_lo;
-    // Work items are 16-byte pieces along the partial's contiguous dimension:
-    // (row, 4 columns) for a row-major output, (column, 4 rows) for a
-    // transposed one; consecutive threads take consecutive pieces, so the
-    // remote reads and the bf16 stores are contiguous.  A thread takes kBatch
-    // pieces at a time and issues all their peer loads (up to 8 peers) before
-    // the first add, so the remote-load latency is paid once per batch; each
-    // piece's partials are added in peer order.
-    constexpr int kBatch = C::NUM_THREADS > 256 ? 1 : 2;   // 32 registers of partials per piece
-    constexpr int kPieces = C::BN / 4;                      // pieces per row (row-major output)
-    const int nel = C::OUT_T ? nu * C::BN : nu * kPieces;
-    const bool vec_ok = (p.out_ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7u) == 0;
-    for (int i0 = threadIdx.x; i0 < nel; i0 += kBatch * C::NUM_THREADS) {
-      float4 part[kBatch][8];
-      int row[kBatch], col[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int i = i0 + b * C::NUM_THREADS;
-        const bool live = i < nel;
-        const int ii = live ? i : 0;
-        uint32_t off;
-        if (!C::OUT_T) {
-          row[b] = u_lo + ii / kPieces;
-          col[b] = 4 * (ii % kPieces);
-          off = base + (static_cast<uint32_t>(row[b]) * C::PART_LD + static_cast<uint32_t>(col[b])) * 4u;
-        } else {
-          row[b] = 4 * (u_lo + ii % nu);
-          col[b] = ii / nu;
-          off = base + (static_cast<uint32_t>(col[b]) * 128u + static_cast<uint32_t>(row[b])) * 4u;
-        }
-        if (!live) col[b] = -1;
-#pragma unroll
-        for (int pr = 0; pr < 8; ++pr)
-          part[b][pr] = (live && static_cast<uint32_t>(pr) < size) ? ld_dsmem_v4(off, static_cast<uint32_t>(pr))
-                                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (col[b] < 0) continue;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int pr = 0; pr < 8; ++pr) {
-          if (static_cast<uint32_t>(pr) < size) {
-            acc.x += part[b][pr].x;
-            acc.y += part[b][pr].y;
-            acc.z += part[b][pr].z;
-            acc.w += part[b][pr].w;
-          }
-        }
-        const int64_t grow = static_cast<int64_t>(m_tile) * C::BM + row[b];
-        const int64_t gcol = static_cast<int64_t>(n_tile) * C::BN + col[b];
-        const uint32_t h01 = pack_bf16x2(acc.x * p.alpha, acc.y * p.alpha);
-        const uint32_t h23 = pack_bf16x2(acc.z * p.alpha, acc.w * p.alpha);
-        const uint16_t h[4] = {static_cast<uint16_t>(h01 & 0xFFFFu), static_cast<uint16_t>(h01 >> 16),
-                               static_cast<uint16_t>(h23 & 0xFFFFu), static_cast<uint16_t>(h23 >> 16)};
-        if (!C::OUT_T) {
-          // Row grow, columns gcol .. gcol + 3.
-          if (grow >= p.out_rows) continue;
-          if (vec_ok && gcol + 4 <= p.out_cols) {
-            *reinterpret_cast<uint2 *>(p.out + grow * p.out_ld + gcol) = make_uint2(h01, h23);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (gcol + e < p.out_cols) p.out[grow * p.out_ld + gcol + e] = h[e];
-          }
-        } else {
-          // Column gcol of the tile = row gcol of the transposed output, its
-          // entries grow .. grow + 3.
-          if (gcol >= p.out_cols) continue;
-          if (vec_ok && grow + 4 <= p.out_rows) {
-            *reinterpret_cast<uint2 *>(p.out + gcol * p.out_ld + grow) = make_uint2(h01, h23);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (grow + e < p.out_rows) p.out[gcol * p.out_ld + grow + e] = h[e];
-          }
-        }
-      }
-    }
+    split_reduce<C::BN, C::NUM_THREADS, C::OUT_T>(base, C::PART_LD, p.out, p.out_ld, p.out_rows, p.out_cols,
+                                                  static_cast<int64_t>(m_tile) * C::BM,
+                                                  static_cast<int64_t>(n_tile) * C::BN, p.alpha);
     cluster_sync_all();
   }
   tc_fence_before();
@@ -622,20 +611,6 @@ cudaError_t launch(const TcParams &p, int grid_n, int grid_m, cudaStream_t strea
   return e;
 }
 
-// Split of the contraction for a product with `tiles` output tiles and
-// `ksteps` k-steps: fill about `per_sm` CTAs per SM (two for the skinny
-// products, which fit two to an SM; one for the input gradient), at least two
-// k-steps per CTA, at most 8 CTAs per cluster.
-int choose_split(int64_t tiles, int ksteps, int per_sm = 2) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int64_t sp = (static_cast<int64_t>(per_sm) * sms) / (tiles > 0 ? tiles : 1);
-  if (sp > 8) sp = 8;
-  if (sp > ksteps / 2) sp = ksteps / 2;
-  return sp < 1 ? 1 : static_cast<int>(sp);
-}
-
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 using CfgFwd1 = Cfg<256, 1, false, true, false, false>;
@@ -647,8 +622,26 @@ using CfgProjMN = Cfg<64, 1, false, false, true, false, true>;
 using CfgTN = Cfg<64, 1, true, false, true, false, true>;
 using CfgTNT = Cfg<64, 1, true, false, true, true, true>;
 using CfgDropAdd = Cfg<256, 1, false, false, true, false, false, kEpiDropoutAdd>;
+using CfgFwd1M = Cfg<256, 1, false, true, false, false, false, kEpiStore, true>;
+using CfgFwd1SM = Cfg<256, 1, false, true, false, false, true, kEpiStore, true>;
+using CfgBwd1M = Cfg<256, 1, false, true, true, false, false, kEpiStore, true>;
+using CfgBwd1SM = Cfg<256, 1, false, true, true, false, true, kEpiStore, true>;
 
 }  // namespace
+
+// Split of the contraction for a product with `tiles` output tiles and
+// `ksteps` k-steps: fill about `per_sm` CTAs per SM (two for the skinny
+// products, which fit two to an SM; one for the input gradient), at least two
+// k-steps per CTA, at most 8 CTAs per cluster.
+int choose_split(int64_t tiles, int ksteps, int per_sm) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int64_t sp = (static_cast<int64_t>(per_sm) * sms) / (tiles > 0 ? tiles : 1);
+  if (sp > 8) sp = 8;
+  if (sp > ksteps / 2) sp = ksteps / 2;
+  return sp < 1 ? 1 : static_cast<int>(sp);
+}
 
 cudaError_t tc_fwd(const uint16_t *X, int64_t m, const WeightView &w, const uint16_t *T, const uint16_t *B,
                    int32_t r, uint16_t *Y, cudaStream_t stream, bool pdl) {
@@ -720,6 +713,39 @@ cudaError_t tc_bwd_dx(const uint16_t *dY, int64_t m, const WeightView &w, const 
   const int sp = choose_split(int64_t(gn) * gm, p.num_main, 1);
   return sp > 1 ? launch<CfgBwd1S>(p, gn, gm, stream, sp, p.pdl != 0)
                 : launch<CfgBwd1>(p, gn, gm, stream, 1, p.pdl != 0);
+}
+
+cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
+                     const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream) {
+  if (m > 128) return fused_multi_large(L, m, w, bwd, V, ad, lists, out, stream);
+  TcParams p{};
+  const int64_t in = bwd ? w.n : w.k, cols = bwd ? w.k : w.n;
+  const uint32_t width = static_cast<uint32_t>(unit_width(ad.r));
+  if (!encode_bf16_map(&p.tmA, L, m, in, 64, 128)) return cudaErrorInvalidValue;
+  if (!encode_codes_map(&p.tmCodes, w.codes, w.n, w.k / 2, 32, bwd ? 64 : 256, false)) return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, width, 128)) return cudaErrorInvalidValue;
+  if (bwd ? !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)
+          : !encode_bf16_stack_map(&p.tmB2, ad.B, ad.count, w.n, ad.r, width, 256))
+    return cudaErrorInvalidValue;
+  p.absmax_q = w.absmax_q;
+  p.group_scale = w.group_scale;
+  p.mu = w.mu;
+  p.out = out;
+  p.err = device_error_word();
+  p.w_n = w.n;
+  p.w_k = w.k;
+  p.out_ld = cols;
+  p.out_rows = static_cast<int>(m);
+  p.out_cols = static_cast<int>(cols);
+  p.num_main = cdiv(in, 64);
+  p.num_lora = 0;
+  p.alpha = 1.0f;
+  p.tab = *w.tab;
+  p.multi = multi_params(ad, lists);
+  const int gn = cdiv(cols, 256);
+  const int sp = choose_split(gn, p.num_main, 1);
+  if (bwd) return sp > 1 ? launch<CfgBwd1SM>(p, gn, 1, stream, sp, true) : launch<CfgBwd1M>(p, gn, 1, stream, 1, true);
+  return sp > 1 ? launch<CfgFwd1SM>(p, gn, 1, stream, sp, true) : launch<CfgFwd1M>(p, gn, 1, stream, 1, true);
 }
 
 cudaError_t tc_proj_kmajor(const uint16_t *L, int64_t m, int64_t kc, const uint16_t *R, int32_t r, float scale,

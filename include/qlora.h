@@ -24,7 +24,10 @@
  * _noalloc form), qlora_linear_bwd_dx, qlora_lora_bwd (adapter gradients),
  * qlora_linear_bwd (the whole backward, rank-r intermediates formed once),
  * qlora_merge_adapter (W^ + s B A for export), qlora_lora_dropout and the
- * _dropout forms of the forward and input gradient; helpers for workspace sizes,
+ * _dropout forms of the forward and input gradient; qlora_linear_fwd_multi /
+ * qlora_linear_bwd_multi (rows of many adapters on one weight),
+ * qlora_act_quantize / qlora_act_dequant / qlora_linear_bwd_act8 (8-bit
+ * activation checkpoints); helpers for workspace sizes,
  * codebook levels, errors, versions and launch counts.
  *
  * Conventions for every entry point
@@ -34,7 +37,8 @@
  *   - Matrices are dense row-major.  bf16 tensors are passed as uint16_t bit
  *     patterns (the layout of __nv_bfloat16).  W is [n x k] (out x in),
  *     X [m x k], Y [m x n], A [r x k], B [n x r].
- *   - Every tensor pointer must be 16-byte aligned.
+ *   - Every tensor pointer must be 16-byte aligned (row ids and adapter scales:
+ *     4-byte).
  *   - Shapes: n > 0, k > 0, k % 64 == 0; the linear operations also need
  *     n % 8 == 0 (16-byte bf16 rows of Y and dY);
  *     r % 16 == 0 with 0 <= r <= 256 (r == 0, or A == B == NULL, means no
@@ -298,6 +302,99 @@ int qlora_linear_bwd_dx_dropout(const uint16_t *dY, int64_t m, const qlora_nf4_w
                                 const uint16_t *A, const uint16_t *B, int32_t r, float scale,
                                 float p, uint64_t seed, uint64_t offset, uint16_t *dX,
                                 void *ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* 8-bit activation checkpoints.  What a layer keeps of its input between the
+ * forward and the backward serves one product, dA = U^T X ["QLoRA and
+ * Quantized Training", The idea (only the adapters hold gradients)], and is
+ * the layer's largest activation.  The pages give no format for it; this one
+ * stores X [m x k] bf16 in 1.03 bytes per element.  Per block of 64
+ * consecutive elements of a row:
+ *     c     = max |x|,   scale = bf16_rne(c / 127)
+ *     codes = clamp(rint_even(x / scale), -127, 127)     (0 when scale == 0)
+ *     X^    = bf16_rne(codes . scale)
+ * so |X^ - x| <= scale / 2 plus one bf16 rounding.  x is finite and below
+ * 2^127 in magnitude.
+ *   codes  int8 [m x k] row-major;  scale  bf16 [m x k/64];  m >= 0, k % 64 == 0
+ * One checkpoint serves every layer with the same input (q, k and v).        */
+typedef struct {
+  const int8_t *codes;
+  const uint16_t *scale;
+  int64_t m, k;
+} qlora_act8;
+
+/* X bf16 [m x k] -> codes, scale. */
+int qlora_act_quantize(const uint16_t *X, int64_t m, int64_t k, int8_t *codes, uint16_t *scale,
+                       qlora_stream_t stream);
+/* X^ bf16 [m x k] of a checkpoint. */
+int qlora_act_dequant(const qlora_act8 *x, uint16_t *X, qlora_stream_t stream);
+
+/* qlora_linear_bwd with X read from a checkpoint of it (with dropout: of Xd):
+ *   dX, dB  as qlora_linear_bwd;   dA = bf16(U^T . X^)
+ * T is required (the forward's: it saw X itself).  x8->m == m and x8->k == w->k,
+ * else QLORA_ERR_SHAPE.  ws >= qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, r).
+ * m == 0 writes zeros to dA and dB and reads neither x8 nor T.               */
+int qlora_linear_bwd_act8(const uint16_t *dY, const qlora_act8 *x8, const uint16_t *T, int64_t m,
+                          const qlora_nf4_weight *w, const uint16_t *A, const uint16_t *B, int32_t r,
+                          float scale, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes,
+                          qlora_stream_t stream);
+
+/* Many adapters on one frozen weight ["QLoRA", Training setup versus
+ * deployment setup (serve the quantized base with the adapter)]: each row of a
+ * batch has its own adapter.
+ *   A     bf16 [count x r x k],  B  bf16 [count x n x r]  (adapters of a lower
+ *         rank are padded with zero rows of A and zero columns of B)
+ *   scale fp32 [count], s_a = alpha_a / r_a, DEVICE memory
+ *   0 < r <= 256, r % 16 == 0;  0 < count <= QLORA_MULTI_MAX_ADAPTERS
+ * `ids` int32 [m] (device) names each row's adapter, in any order; an id
+ * outside [0, count) means none: the row gets the frozen product alone and
+ * adds to no gradient.  scale and ids need 4-byte alignment only.  The ids are
+ * read on the device, so a captured call follows their contents.
+ * m <= QLORA_MULTI_MAX_ROWS.
+ *
+ * Rows of one adapter that lie together cost least (their products share
+ * tiles); any order is correct, and no row's result depends on another
+ * adapter's rows or values.  Results do not depend on timing (no
+ * floating-point atomics).                                                   */
+#define QLORA_MULTI_MAX_ADAPTERS 65535
+#define QLORA_MULTI_MAX_ROWS (1 << 22)
+typedef struct {
+  const uint16_t *A;
+  const uint16_t *B;
+  const float *scale;
+  int32_t count;
+  int32_t r;
+} qlora_adapter_set;
+
+/* Forward: Y[i] = bf16( X[i] . W^T + T[i] . B_a^T ),  T[i] = bf16(s_a . X[i] . A_a^T),
+ * a = ids[i].
+ *   X bf16 [m x k], Y bf16 [m x n]; w, n, k as in qlora_linear_fwd
+ *   ws  scratch, ws_bytes >= qlora_multi_workspace_bytes(QLORA_OP_FWD, m, n, k, r, count);
+ *       afterwards its first m*r*2 bytes hold T [m x r] (zero rows where there
+ *       is no adapter), which qlora_linear_bwd_multi takes.
+ * m <= 16 runs the weight-streaming kernels, larger m the tcgen05 kernels, as
+ * in qlora_linear_fwd.                                                       */
+int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight *w,
+                           const qlora_adapter_set *adapters, const int32_t *ids, uint16_t *Y, void *ws,
+                           size_t ws_bytes, qlora_stream_t stream);
+
+/* Backward: with a = ids[i] and U[i] = bf16(s_a . dY[i] . B_a),
+ *   dX[i] = bf16( dY[i] . W^ + U[i] . A_a )             (skipped when dX is NULL)
+ *   dA_a  = bf16( sum over a's rows of U[i]^T . X[i] )  [count x r x k]
+ *   dB_a  = bf16( sum over a's rows of dY[i]^T . T[i] ) [count x n x r]
+ * X is given as bf16 (x8 NULL) or as its checkpoint (X NULL; X^ takes its
+ * place): exactly one of the two, else QLORA_ERR_NULL.  T is the forward's, or
+ * NULL to compute it here from X (not from a checkpoint).  dA and dB are
+ * overwritten for every adapter; one without rows gets zeros.
+ *   ws >= qlora_multi_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, r, count)
+ * m == 0 writes zeros to dA and dB.                                          */
+int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_act8 *x8, const uint16_t *T,
+                           int64_t m, const qlora_nf4_weight *w, const qlora_adapter_set *adapters,
+                           const int32_t *ids, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws,
+                           size_t ws_bytes, qlora_stream_t stream);
+
+/* Workspace bytes of the two calls above (op QLORA_OP_FWD / QLORA_OP_LORA_BWD);
+ * SIZE_MAX for another op or invalid sizes.                                  */
+size_t qlora_multi_workspace_bytes(int op, int64_t m, int64_t n, int64_t k, int32_t r, int32_t count);
 
 /* Forward with no caller workspace, for callers that cannot allocate device
  * memory: code whose host owns every device allocation (an engine plugin), a
