@@ -493,16 +493,16 @@ class Act8:
         return self.codes.numel() + 2 * self.scale.numel()
 
 
-def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device) -> None:
-    """The tensor is a contiguous CUDA tensor of this type, shape and device."""
-    if t is None:
+def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device: torch.device) -> None:
+    """The tensor is a contiguous tensor of this type and shape on this CUDA
+    device."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device and t.is_cuda):
         return
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors")
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)}, not {t.dtype} {list(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _need_act8(act: Act8, m: int, k: int, device) -> None:
@@ -518,17 +518,17 @@ def _need_weight(w: NF4Weight, device) -> None:
 
 
 def _need_ws(ws: Optional[torch.Tensor], device) -> None:
-    _need_cuda(ws)
-    if ws is not None and ws.device != device:
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        _need_cuda(ws)
         raise ValueError(f"ws is on {ws.device}, not on {device}")
 
 
 def _stream_on(device: torch.device, stream) -> Optional[int]:
     """The stream's handle; the default is the current stream of the tensors'
     device, which must be the current device (the library launches there)."""
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
 
 
 def qlora_act_quantize(X: torch.Tensor, out: Optional[Act8] = None, stream=None) -> Act8:
@@ -537,7 +537,7 @@ def qlora_act_quantize(X: torch.Tensor, out: Optional[Act8] = None, stream=None)
     if X.dim() != 2 or X.shape[1] % BLOCK:
         raise ValueError("X must be a 2-D tensor with a row length that is a multiple of 64")
     m, k = X.shape
-    _need(X, "X", torch.bfloat16, (m, k), None)
+    _need(X, "X", torch.bfloat16, (m, k), X.device)
     if out is None:
         out = Act8.empty(m, k, X.device)
     _need_act8(out, m, k, X.device)

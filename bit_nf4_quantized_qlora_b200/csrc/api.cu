@@ -274,7 +274,7 @@ int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, cons
   if (e == cudaSuccess) e = prof_mark(t_prof_stop, s);
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
   if (e == cudaSuccess)
-    e = X8 ? launch_group_grads(nullptr, &x8, m, k, U, r, nullptr, dA, true, s)
+    e = X8 ? launch_group_grads(nullptr, &x8, U, k, dA, nullptr, nullptr, 0, nullptr, m, r, nullptr, s)
            : tc_tn_skinny(X, m, k, U, r, dA, true, s);                                    // dA = U^T X
   if (e == cudaSuccess && !one_pass) e = tc_tn_skinny(dY, m, n, T ? T : Tw, r, dB, false, s);   // dB = dY^T T
   return cuda_status(e);
@@ -617,8 +617,9 @@ int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight 
     if (e == cudaSuccess) e = launch_small_m(X, m, w, T, a->B, a->r, Y, s, true, ids, a->count);
   } else {
     const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
-    const TileLists lists = carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count);
-    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, s);
+    const TileLists lists =
+        carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count, multi_tile_rows(m, w->n, w->k / 64));
+    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, nullptr, s);
     if (e == cudaSuccess) e = tc_multi(X, m, view(w), false, T, ad, lists, Y, s);
   }
   return cuda_status(e);
@@ -659,15 +660,15 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
   uint8_t *p = static_cast<uint8_t *>(ws);
   uint16_t *U = reinterpret_cast<uint16_t *>(p), *Tw = reinterpret_cast<uint16_t *>(p + mr);
-  const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count);
-  const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(static_cast<size_t>(lists.bytes)), m, a->count);
-  cudaError_t e = launch_group_rows(ids, m, rows, s);
-  if (e == cudaSuccess && !T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, s);   // T = s_a X A_a^T
-  if (e == cudaSuccess) e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, s);   // U = s_a dY B_a
-  if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);     // dX = dY W^ + U A_a
+  const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, (n + 63) / 64));
+  const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), m, a->count);
+  cudaError_t e = cudaSuccess;
+  if (!T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, nullptr, s);                          // T = s_a X A_a^T
+  if (e == cudaSuccess) e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, &rows, s);  // U = s_a dY B_a
+  if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);                 // dX = dY W^ + U A_a
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
-  if (e == cudaSuccess) e = launch_group_grads(X, X8 ? &x8 : nullptr, m, k, U, a->r, &rows, dA, true, s);
-  if (e == cudaSuccess) e = launch_group_grads(dY, nullptr, m, n, T ? T : Tw, a->r, &rows, dB, false, s);
+  if (e == cudaSuccess)
+    e = launch_group_grads(X, X8 ? &x8 : nullptr, U, k, dA, dY, T ? T : Tw, n, dB, m, a->r, &rows, s);
   return cuda_status(e);
 }
 

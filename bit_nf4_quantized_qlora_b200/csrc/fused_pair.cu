@@ -196,46 +196,50 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
       }
     }
     if constexpr (MULTI) {
-      // 64 / width units a step: this CTA's rows of T (or U) at the unit's
-      // rank columns, and its half of the adapter matrix.  The whole warp
-      // walks the list, lane 0 issues.
-      griddep_wait();
-      const MultiTile t = multi_tile(p.multi, m_pair);
-      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
-      const uint32_t w = static_cast<uint32_t>(p.multi.width);
-      const int units = t.adapters * per_adapter;
+      // Adapter k-steps of the tile's list.  This CTA's rows of a rank block
+      // of T or U go into each activation slot once; the input gradient's
+      // adapter rows come by TMA, the forward's from the dequant warps.  The
+      // whole warp walks the list, lane 0 issues.  While lane 0 is in the main
+      // loop the others bring the adapters' rows to L2.
       AdapterWindow win;
+      const MultiTile t = multi_open(p.multi, m_pair, win, [&](int a) {
+        prefetch_adapter(p.multi, BWD, a, c0, kHalfN, p.out_cols);
+      });
+      const MultiSteps steps(p.multi, t);
+      const int n_steps = steps.count();
       int ok = __shfl_sync(0xffffffffu, issued, 0) == total;
-      for (int u0 = 0, it = total; u0 < units && ok; u0 += per_step, ++it) {
-        const int s = it % kStages;
+      MultiStep at(steps, 0);
+      for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
+        const int it = total + st, s = it % kStages;
         const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
         const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
         const uint32_t xbar = mapa_shared(smem_u32(&xfull[s]), 0);
-        const int nu = units - u0 < per_step ? units - u0 : per_step;
+        MultiStep step = at;
+        const bool fresh = step.since < kStages;
         if (lane == 0) {
           ok = mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(it / kStages) & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
           if (ok) {
-            if (leader) mbar_arrive_expect_tx(&xfull[s], static_cast<uint32_t>(nu) * w * 2u * (512u + 256u));
+            if (leader)
+              mbar_arrive_expect_tx(&xfull[s], 2u * ((fresh ? kABytes : 0u) +
+                                                     (BWD ? (static_cast<uint32_t>(step.units) << steps.lw) * 256u : 0u)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int y = (m0 + h * 128 < p.m) ? m0 + h * 128 : 0;
+              if (fresh) tma_load_2d_pair(xa + h * kASub, &p.tmA2, xbar, step.block * kBK, y);
+            }
             ++issued;
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        for (int u = 0; u < nu; ++u) {
-          const int a = win.at(t, (u0 + u) / per_adapter), c = ((u0 + u) % per_adapter) * p.multi.width;
-          if (lane == 0 && ok) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int y = (m0 + h * 128 < p.m) ? m0 + h * 128 : 0;
-              tma_load_2d_pair(xa + h * kASub + u * 256u * w, &p.tmA2, xbar, c, y);
-            }
-            if (!BWD) {
-              tma_load_3d_pair(wb + u * 256u * w, &p.tmB2, xbar, c, (c0 < p.n) ? static_cast<int>(c0) : 0, a);
-            } else {
+        if (BWD) {
+          for (int u = 0; u < step.units; ++u, step.advance()) {
+            const int a = win.at(t, step.slot), c = step.block * 64 + (step.sub << steps.lw);
+            if (lane == 0 && ok) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const int64_t col = c0 + 64 * j;
-                tma_load_3d_pair(wb + j * 8192u + u * 128u * w, &p.tmB2, xbar, col < p.k ? static_cast<int>(col) : 0, c,
-                                 a);
+                tma_load_3d_pair(wb + j * 8192u + (static_cast<uint32_t>(u) << steps.lw) * 128u, &p.tmB2, xbar,
+                                 col < p.k ? static_cast<int>(col) : 0, c, a);
               }
             }
           }
@@ -301,37 +305,40 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     }
     if constexpr (MULTI) {
       if (leader) {
-        griddep_wait();
-        const MultiTile t = multi_tile(p.multi, m_pair);
-        const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
-        const uint32_t w = static_cast<uint32_t>(p.multi.width);
-        const int units = t.adapters * per_adapter;
         MaskWindow<4> win;
+        const MultiTile t = multi_open(p.multi, m_pair, win, [](int) {});
+        const MultiSteps steps(p.multi, t);
+        const uint32_t w = 1u << steps.lw;
+        const int n_steps = steps.count();
+        MultiStep at(steps, 0);
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        for (int u0 = 0, it = total; u0 < units && ok; u0 += per_step, ++it) {
-          const int s = it % kStages;
+        for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
+          const int it = total + st, s = it % kStages;
+          const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
           const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
           const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
-          const int nu = units - u0 < per_step ? units - u0 : per_step;
-          if (lane == 0)
-            ok = mbar_wait_cluster_bounded(&xfull[s], static_cast<uint32_t>(it / kStages) & 1u, p.err, kErrTimeoutFullA);
+          if (lane == 0) {
+            ok = mbar_wait_cluster_bounded(&xfull[s], ph, p.err, kErrTimeoutFullA);
+            if (ok && !BWD) ok = mbar_wait_cluster_bounded(&wfull[s], ph, p.err, kErrTimeoutFullB);
+          }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           if (lane == 0) tc_fence_after();
-          for (int u = 0; u < nu; ++u) {
-            win.load(t, (u0 + u) / per_adapter);
+          MultiStep step = at;
+          const uint64_t ad = smem_desc(xa, 16u, 1024u);
+          const uint64_t bd = BWD ? smem_desc(wb, 8192u, 1024u) : smem_desc_unit(wb, 16u, 16u * w, static_cast<int>(w));
+          for (int u = 0; u < step.units; ++u, step.advance()) {
+            win.load(t, step.slot);
             if (lane == 0) {
+              // Offsets in the descriptors' 16-byte units.
+              const uint64_t ua = ad + ((static_cast<uint32_t>(step.sub) << steps.lw) >> 3);
+              const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (BWD ? 8u : 16u);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                for (uint32_t kk = 0; kk < w / 16u; ++kk) {
-                  const uint64_t ad =
-                      smem_desc_unit(xa + h * kASub + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
-                  const uint64_t bd = BWD ? smem_desc(wb + u * 128u * w + kk * 2048u, 8192u, 1024u)
-                                          : smem_desc_unit(wb + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
-                  // Rows 128 h .. of the even CTA's 256, then of the odd CTA's.
-                  umma_f16_pair_masked(tmem + static_cast<uint32_t>(h * kBN), ad, bd, kIdesc, win.off[h],
-                                       win.off[2 + h]);
-                }
+              for (uint32_t h = 0; h < 2; ++h) {
+                // Rows 128 h .. of the even CTA's 256, then of the odd CTA's.
+                for (uint32_t kk = 0; kk < w / 16u; ++kk)
+                  umma_f16_pair_masked(tmem + h * kBN, ua + h * (kASub / 16u) + kk * 2u, ub + kk * (BWD ? 128u : 2u),
+                                       kIdesc, win.off[h], win.off[2 + h]);
               }
             }
           }
@@ -380,8 +387,21 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     float S_nx = blk_nx >= 0 ? __ldg(p.group_scale + (blk_nx >> 8)) : 0.f;
     int64_t g_cur = -1;
     float t_cur = 0.f;
+    // Many adapters: the tile's list is requested two of the group's steps
+    // before the main loop ends.
+    AdapterWindow win;
+    int adapters = -1;
+    const auto open_list = [&]() {
+      if (adapters >= 0) return;
+      griddep_wait();
+      adapters = __ldcg(multi_tile_at(p.multi, m_pair));
+      win.prime(p.multi, multi_tile_at(p.multi, m_pair));
+    };
     for (int it = grp; it < total; it += kGroups) {
       const uint32_t use = static_cast<uint32_t>(it / kStages);
+      if constexpr (MULTI && !BWD) {
+        if (it + 2 * kGroups >= total) open_list();
+      }
       if (it < p.num_main) {
         const int c = it % kCodeSlots;
         if (!mbar_wait_bounded(&cfull[c], static_cast<uint32_t>(it / kCodeSlots) & 1u, p.err, kErrTimeoutFullA))
@@ -436,6 +456,30 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
         blk_nx = block_of(it + kGroups);
         q_nx = blk_nx >= 0 ? __ldg(p.absmax_q + blk_nx) : 0u;
         S_nx = blk_nx >= 0 ? __ldg(p.group_scale + (blk_nx >> 8)) : 0.f;
+      }
+    }
+    if constexpr (MULTI && !BWD) {
+      // The adapter k-steps' rows of B_a (this CTA's half tile), requested a
+      // step of the group ahead.
+      open_list();
+      const MultiTile t = multi_tile_of(p.multi, multi_tile_at(p.multi, m_pair), adapters);
+      const MultiSteps steps(p.multi, t);
+      const int n_steps = steps.count();
+      int st = ((grp - total % kGroups) + kGroups) % kGroups;
+      MultiStep at(steps, 0);
+      for (int i = 0; i < st; ++i) at.next(steps);
+      MultiRows<kHalfN> rows;
+      if (st < n_steps) rows.load(p.multi, at, win, t, p.n, c0, dt);
+      for (; st < n_steps; st += kGroups) {
+        const uint32_t use = static_cast<uint32_t>((total + st) / kStages);
+        const bool free_slot = mbar_wait_bounded(&empty[grp], (use & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
+        if (!__all_sync(0xffffffffu, free_slot)) break;
+        rows.store(p.multi, wslot, dt);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(wbar);
+        for (int i = 0; i < kGroups; ++i) at.next(steps);
+        if (st + kGroups < n_steps) rows.load(p.multi, at, win, t, p.n, c0, dt);
       }
     }
 
@@ -579,10 +623,8 @@ cudaError_t fused_multi_large(const uint16_t *L, int64_t m, const WeightView &w,
   const uint32_t width = static_cast<uint32_t>(unit_width(ad.r));
   if (!encode_bf16_map(&p.tmA, L, m, in, 64, 128)) return cudaErrorInvalidValue;
   if (!encode_codes_map(&p.tmCodes, w.codes, w.n, w.k / 2, 32, bwd ? 64 : kHalfN, false)) return cudaErrorInvalidValue;
-  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, width, 128)) return cudaErrorInvalidValue;
-  if (bwd ? !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)
-          : !encode_bf16_stack_map(&p.tmB2, ad.B, ad.count, w.n, ad.r, width, kHalfN))
-    return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, 64, 128)) return cudaErrorInvalidValue;
+  if (bwd && !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)) return cudaErrorInvalidValue;
   if (!encode_bf16_map(&p.tmOut, out, m, cols, 64, 256)) return cudaErrorInvalidValue;
   p.out_cols = cols;
   p.num_main = static_cast<int>((in + kBK - 1) / kBK);

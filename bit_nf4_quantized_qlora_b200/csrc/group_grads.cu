@@ -10,19 +10,27 @@
 // several adapters, so a batch holds the rows of several.
 //
 // The contraction runs over a group's rows, wherever in the batch they are.
-// group_rows_kernel writes each group's row numbers in ascending order, padded
-// to whole steps of 64; a step whose rows are consecutive is one TMA box, any
-// other is sixteen row-gathering TMA loads of four rows.  So the work is the
-// rows themselves (plus the last step's padding), in every order of the batch,
-// and a group never reads another group's rows.  The pad rows of the last
-// step repeat one of the group's own rows and are zeroed in R's tile before
-// the product.
+// multi_proj.cu writes each group's row numbers in ascending order into
+// slots of 64 (a group starts on a slot of its own); a slot whose rows are
+// consecutive is one TMA box, any other is sixteen row-gathering TMA loads of
+// four rows.  So the work is the rows themselves (plus the last slot's
+// padding), in every order of the batch, and a group never reads another
+// group's rows.  The pad rows of a group's last slot repeat one of its own rows
+// and are zeroed in R's tile before the product.
 //
-// One CTA per (128 columns of L, 64 columns of R, group), the rows split over
-// a cluster of up to 8 CTAs when the tiles alone cannot fill the SMs; fp32
-// partials are added in rank order, so results do not depend on timing.  An
-// M = 128, N = 64 product of K = 64 rows reads 16 KB of L: the kernel is
-// bound by reading L once per 64 ranks (HBM, or L2 for r > 64).
+// A CTA takes 128 columns of L, 64 columns of R and an equal share of the
+// slots, whatever groups they belong to: a cluster of up to 8 CTAs covers all
+// slots, as many as it takes to fill the SMs.  Inside its share it walks the
+// groups with two accumulators in tensor memory, so the next group's products
+// run while the last one's result is written.  Only a group that crosses the
+// border of two shares is reduced across the cluster (its partials wait in
+// tensor memory until the end, then go through distributed shared memory, in
+// rank order: results do not depend on timing).  So the time follows the number
+// of rows and not how they are spread over the groups.
+//
+// An M = 128, N = 64 product of K = 64 rows reads 16 KB of L: the kernel is
+// bound by reading L once per 64 ranks (HBM, or L2 for r > 64) and, for many
+// small groups, by writing their results.
 //
 // Checkpoint form: L's tile arrives as 64 x 128 codes (half the bytes); the
 // four epilogue warps expand it to the bf16 tile the product reads, one block
@@ -38,21 +46,27 @@
 namespace qlora {
 namespace {
 
-constexpr int kStep = 64;                 // rows of a step
+constexpr int kSlot = 64;                 // rows of a step
 constexpr int kThreads = 192;             // TMA warp, MMA warp, four expand / epilogue warps
-constexpr uint32_t kLBytes = 128u * kStep * 2u;   // bf16 tile: two 64-column slabs
-constexpr uint32_t kRBytes = 64u * kStep * 2u;
-constexpr uint32_t kCBytes = 128u * kStep;        // code tile
+constexpr uint32_t kLBytes = 128u * kSlot * 2u;   // bf16 tile: two 64-column slabs
+constexpr uint32_t kRBytes = 64u * kSlot * 2u;
+constexpr uint32_t kCBytes = 128u * kSlot;        // code tile
 constexpr uint32_t kPartLd = 64u + 4u;
+constexpr uint32_t kPartBytes = 128u * kPartLd * 4u;
+// Accumulators: two in turn, and one for the group that began in an earlier
+// share, which keeps its partial until the end.
+constexpr uint32_t kLeftAcc = 2u;
+constexpr uint32_t kTmemCols = 256u;
 
 template <bool ACT8>
 constexpr int stages() { return ACT8 ? 3 : 4; }
 template <bool ACT8>
 constexpr uint32_t stage_bytes() { return kLBytes + kRBytes + (ACT8 ? kCBytes : 0u); }
-template <bool ACT8>
-constexpr uint32_t smem_bytes() { return stage_bytes<ACT8>() * stages<ACT8>() + 1024u; }
-static_assert(2u * smem_bytes<false>() <= 227u * 1024u && 2u * smem_bytes<true>() <= 227u * 1024u, "two CTAs per SM");
-static_assert(stage_bytes<true>() * stages<true>() >= 128u * kPartLd * 4u, "room for the fp32 partial tile");
+constexpr uint32_t kRing = stage_bytes<false>() * stages<false>();
+constexpr uint32_t kSmem = kRing + 1024u;
+static_assert(kRing == stage_bytes<true>() * stages<true>(), "the two forms share a kernel");
+static_assert(2u * (kSmem + 2048u) <= 227u * 1024u, "two CTAs per SM");
+static_assert(kRing >= 2u * kPartBytes, "room for two fp32 partial tiles");
 
 struct __align__(64) GroupParams {
   CUtensorMap tmL, tmLg;        // L by boxes of 64 rows / by single rows
@@ -63,30 +77,154 @@ struct __align__(64) GroupParams {
   uint16_t *out;                // [groups x P x r], or [groups x r x P] transposed
   unsigned *err;
   int64_t P;
-  int m, r, rtiles;
+  int m, r, rtiles, groups;
 };
 
+// A CTA's part of a group: slots [b, e) of the group's [s, s + slots()).
+struct Part {
+  int group, s, rows, b, e;
+  __device__ __forceinline__ int slots() const { return (rows + kSlot - 1) / kSlot; }
+  __device__ __forceinline__ bool live() const { return b < e; }
+  __device__ __forceinline__ bool from_left() const { return b > s; }
+  __device__ __forceinline__ bool to_right() const { return e < s + slots(); }
+};
+
+// Walks the groups whose first slot or any slot lies in [lo, hi), by whole
+// warps; lane l holds group base + l.  Groups' first slots ascend strictly.
+struct GroupWalk {
+  const int32_t *start, *count;
+  int groups, lo, hi, m;
+  int a, base, s, c;
+  __device__ __forceinline__ void window(int first) {
+    base = first;
+    const int g = first + static_cast<int>(lane_id());
+    const bool in = g < groups;
+    s = !in ? 0x7FFFFFFF : (start ? __ldg(start + g) / kSlot : 0);
+    c = !in ? 0 : (start ? __ldg(count + g) : m);
+  }
+  __device__ __forceinline__ GroupWalk(const GroupParams &p, int lo_, int hi_)
+      : start(p.list ? p.start : nullptr), count(p.count), groups(p.groups), lo(lo_), hi(hi_), m(p.m) {
+    // The last group that starts at or before lo.
+    int first = 0;
+    for (int span = groups; span > 32;) {
+      const int step = (span + 31) / 32, g = first + static_cast<int>(lane_id()) * step;
+      const bool le = g < first + span && __ldg(start + g) / kSlot <= lo;
+      const int n = __popc(__ballot_sync(0xffffffffu, le));
+      first += (n - 1) * step;
+      span = groups - first < step ? groups - first : step;
+    }
+    window(first);
+    a = first + __popc(__ballot_sync(0xffffffffu, s <= lo)) - 1;
+  }
+  // The next group with slots in the share, or (with `empty`) without rows;
+  // false when there is none.
+  __device__ __forceinline__ bool next(Part *p, bool empty = false) {
+    for (;; ++a) {
+      if (a >= groups) return false;
+      if (a >= base + 32) window(a);
+      const int gs = __shfl_sync(0xffffffffu, s, a - base), gc = __shfl_sync(0xffffffffu, c, a - base);
+      if (gs >= hi) return false;
+      const int end = gs + (gc + kSlot - 1) / kSlot;
+      *p = Part{a, gs, gc, gs > lo ? gs : lo, end < hi ? end : hi};
+      if (p->live() || (empty && gc == 0 && gs >= lo)) {
+        ++a;
+        return true;
+      }
+    }
+  }
+};
+
+// The slots of a share in order.
+struct SlotWalk {
+  GroupWalk walk;
+  Part part{0, 0, 0, 0, 0};
+  __device__ __forceinline__ SlotWalk(const GroupParams &p, int lo, int hi) : walk(p, lo, hi) {}
+  __device__ __forceinline__ int next() {
+    if (part.b >= part.e && !walk.next(&part)) return -1;
+    return part.b++;
+  }
+};
+
+// 64 accumulator columns of this thread's row.
+__device__ __forceinline__ void read_acc(uint32_t tmem, uint32_t acc, int quad, uint32_t (&v)[64]) {
+  uint32_t h[32];
+  tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64u, h);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = h[j];
+  tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64u + 32u, h);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[32 + j] = h[j];
+}
+
+// Writes the thread's row (column p of L) of a group's [128 x 64] result.
+template <bool OUT_T>
+__device__ __forceinline__ void write_result(uint16_t *out, int64_t P, int r, int64_t row, int r0,
+                                             const uint32_t (&v)[64]) {
+  if (!OUT_T) {
+    if (row < P) {
+      uint4 *dst = reinterpret_cast<uint4 *>(out + row * r + r0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r0 + 8 * j < r)
+          dst[j] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
+                              pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
+                              pack_bf16x2(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5])),
+                              pack_bf16x2(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7])));
+    }
+  } else {
+    // Transposed: lanes hold consecutive columns of the output.  Neighbours
+    // exchange one of two rows, so each stores a pair of columns (P is even).
+    const bool odd = lane_id() & 1u;
+#pragma unroll
+    for (int j = 0; j < 64; j += 2) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+      const uint32_t w = odd ? pack_bf16x2(__uint_as_float(got), __uint_as_float(v[j + 1]))
+                             : pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(got));
+      const int64_t rr = r0 + j + (odd ? 1 : 0);
+      if (rr < r && row < P) *reinterpret_cast<uint32_t *>(out + rr * P + (row & ~int64_t(1))) = w;
+    }
+  }
+}
+
+// Puts the thread's row of a partial into shared memory, along the output's
+// contiguous dimension.
+template <bool OUT_T>
+__device__ __forceinline__ void store_partial(uint32_t dst, uint32_t row, const uint32_t (&v)[64]) {
+  if (!OUT_T) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t w[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+      sts128(dst + (row * kPartLd + 4u * static_cast<uint32_t>(j)) * 4u, w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (static_cast<uint32_t>(j) * 128u + row) * 4u), "r"(v[j])
+                   : "memory");
+  }
+}
+
+// One CTA's tile of one product.
 template <bool ACT8, bool OUT_T>
-__global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_constant__ GroupParams p) {
+__device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   constexpr int kStages = stages<ACT8>();
   constexpr uint32_t kStageBytes = stage_bytes<ACT8>();
   constexpr uint32_t kIdesc = make_idesc(64, true, true);
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full[kStages], expanded[kStages], empty[kStages];
-  __shared__ __align__(8) uint64_t acc_bar;
+  __shared__ __align__(8) uint64_t acc_full[3], acc_empty[2];
   __shared__ uint32_t tmem_slot;
+  __shared__ Part left_s, right_s;
 
   const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int p_tile = static_cast<int>(blockIdx.x) / p.rtiles, r_tile = static_cast<int>(blockIdx.x) % p.rtiles;
-  const int group = static_cast<int>(blockIdx.y);
-  const int rows = p.list ? __ldg(p.count + group) : p.m;
-  const int32_t *list = p.list ? p.list + __ldg(p.start + group) : nullptr;
-  const int nsteps = (rows + kStep - 1) / kStep;
+  const int p_tile = tile / p.rtiles, r_tile = tile % p.rtiles;
+  // All slots, and this CTA's share of them.
+  const int slots = p.list ? __ldg(p.start + p.groups - 1) / kSlot + (__ldg(p.count + p.groups - 1) + kSlot - 1) / kSlot
+                           : (p.m + kSlot - 1) / kSlot;
   const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
-  const int s_lo = static_cast<int>((static_cast<int64_t>(nsteps) * z) / nz);
-  const int s_hi = static_cast<int>((static_cast<int64_t>(nsteps) * (z + 1)) / nz);
-  const int n_iters = s_hi - s_lo;
+  const auto share = [&](int i) { return static_cast<int>((static_cast<int64_t>(slots) * i) / nz); };
+  const int lo = share(z), hi = share(z + 1);
   const int p0 = p_tile * 128, r0 = r_tile * 64;
   // Second 64-column slab; past P it repeats the first (its output rows are
   // never stored) and every copy stays in range.
@@ -98,12 +236,14 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
       mbar_init(&expanded[s], 4);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&acc_bar, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&acc_full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 4);
     fence_mbar_init();
+    left_s = right_s = Part{0, 0, 0, 0, 0};
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                 "r"(64u)
+                 "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -114,27 +254,30 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    SlotWalk walk(p, lo, hi);
+    // A slot's rows, four per lane on lanes 0..15; requested a slot ahead.
+    const auto rows_of = [&](int slot) {
+      const int r4 = slot * kSlot + 4 * lane;
+      if (!p.list || slot < 0 || lane >= 16) return make_int4(r4, r4 + 1, r4 + 2, r4 + 3);
+      return __ldg(reinterpret_cast<const int4 *>(p.list + static_cast<int64_t>(slot) * kSlot) + lane);
+    };
     int issued = 0;
-    for (int li = 0; li < n_iters; ++li) {
-      const int s = li % kStages;
-      const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
-      const int row0 = (s_lo + li) * kStep;
-      // The step's rows, four per lane on lanes 0..15.
-      int4 idx = make_int4(row0 + 4 * lane, row0 + 4 * lane + 1, row0 + 4 * lane + 2, row0 + 4 * lane + 3);
-      int first = row0;
-      bool box = true;
-      if (list) {
-        if (lane < 16) idx = __ldg(reinterpret_cast<const int4 *>(list + row0) + lane);
-        first = __shfl_sync(0xffffffffu, idx.x, 0);
-        const int want = first + 4 * lane;
-        const bool in_order = idx.x == want && idx.y == want + 1 && idx.z == want + 2 && idx.w == want + 3;
-        box = __all_sync(0xffffffffu, lane >= 16 || in_order) != 0;
-      }
+    int slot = walk.next();
+    int4 ahead = rows_of(slot);
+    while (slot >= 0) {
+      const int4 idx = ahead;
+      const int s = issued % kStages;
+      slot = walk.next();
+      ahead = rows_of(slot);
+      const int first = __shfl_sync(0xffffffffu, idx.x, 0);
+      const int want = first + 4 * lane;
+      const bool in_order = idx.x == want && idx.y == want + 1 && idx.z == want + 2 && idx.w == want + 3;
+      const bool box = __all_sync(0xffffffffu, lane >= 16 || in_order) != 0;
       int ok = 1;
       const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
       const uint32_t r_s = l_s + kLBytes, c_s = r_s + kRBytes;
       if (lane == 0) {
-        ok = mbar_wait_bounded(&empty[s], ph ^ 1u, p.err, kErrTimeoutEmpty);
+        ok = mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
         if (ok) mbar_arrive_expect_tx(&full[s], (ACT8 ? kCBytes : kLBytes) + kRBytes);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -168,67 +311,132 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
         mbar_wait_bounded(&full[li % kStages], static_cast<uint32_t>(li / kStages) & 1u, p.err, kErrTimeoutDrain);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    int ok = 1;
-    for (int li = 0; li < n_iters; ++li) {
-      const int s = li % kStages;
-      const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
-      const int valid = rows - (s_lo + li) * kStep;
-      const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
-      const uint32_t r_s = l_s + kLBytes;
-      if (lane == 0) {
-        ok = mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA);
-        if (ok && ACT8) ok = mbar_wait_bounded(&expanded[s], ph, p.err, kErrTimeoutFullB);
-      }
+    GroupWalk walk(p, lo, hi);
+    Part part;
+    int ok = 1, li = 0, turn = 0;
+    while (ok && walk.next(&part)) {
+      const bool left = part.from_left();
+      const uint32_t acc = left ? kLeftAcc : static_cast<uint32_t>(turn & 1);
+      if (lane == 0 && !left)
+        ok = mbar_wait_bounded(&acc_empty[acc], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err, kErrTimeoutAcc);
+      if (!left) ++turn;
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (list && valid < kStep) {
-        // Pad rows of the last step: zero rows of R (whole 128-byte rows, so
-        // the swizzle inside them does not matter).
-        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-        for (int c = valid * 8 + lane; c < kStep * 8; c += 32) sts128(r_s + static_cast<uint32_t>(c) * 16u, zero);
-        fence_proxy_async_smem();
+      for (int slot = part.b; slot < part.e && ok; ++slot, ++li) {
+        const int s = li % kStages;
+        const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
+        const int valid = part.rows - (slot - part.s) * kSlot;
+        const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
+        const uint32_t r_s = l_s + kLBytes;
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA);
+          if (ok && ACT8) ok = mbar_wait_bounded(&expanded[s], ph, p.err, kErrTimeoutFullB);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (p.list && valid < kSlot) {
+          // Pad rows of the group's last slot: zero rows of R (whole 128-byte
+          // rows, so the swizzle inside them does not matter).
+          const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+          for (int c = valid * 8 + lane; c < kSlot * 8; c += 32) sts128(r_s + static_cast<uint32_t>(c) * 16u, zero);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const int chunks = valid >= kSlot ? kSlot / 16 : (valid + 15) / 16;
+          uint64_t ld = smem_desc(l_s, 8192u, 1024u), rd = smem_desc(r_s, 8192u, 1024u);
+          umma_f16(tmem + acc * 64u, ld, rd, kIdesc, slot > part.b ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < kSlot / 16; ++kk) {
+            ld += 2048u / 16u;
+            rd += 2048u / 16u;
+            if (kk < chunks) umma_f16(tmem + acc * 64u, ld, rd, kIdesc, 1u);
+          }
+          umma_commit(&empty[s]);
+          if (slot + 1 == part.e) umma_commit(&acc_full[acc]);
+        }
         __syncwarp();
       }
-      if (lane == 0) {
-        tc_fence_after();
-        const int chunks = valid >= kStep ? kStep / 16 : (valid + 15) / 16;
-        for (int kk = 0; kk < chunks; ++kk)
-          umma_f16(tmem, smem_desc(l_s + kk * 2048u, 8192u, 1024u), smem_desc(r_s + kk * 2048u, 8192u, 1024u), kIdesc,
-                   (li > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&empty[s]);
-      }
-      __syncwarp();
     }
-    if (lane == 0 && ok) umma_commit(&acc_bar);
   } else {
     const int t = static_cast<int>(threadIdx.x) - 64;
     bool ok = true;
+    // The expansion and the results share these warps: after a group's last
+    // slot is expanded its result is not waited for until the next group's
+    // slots that fit the ring are expanded too.
+    const int quad = warp & 3;
+    const uint32_t row = static_cast<uint32_t>(quad * 32 + lane);
+    GroupWalk results(p, lo, z + 1 == nz ? 0x7FFFFFFF : hi);
+    int turn = 0;
+    Part part;
+    bool more = results.next(&part, true);
+    int done = 0;            // slots of the groups before `part`
+    // Writes the results of groups whose slots are all among the first
+    // `expanded_slots` of the share.
+    const auto flush = [&](int expanded_slots) {
+      while (ok && more && done + (part.live() ? part.e - part.b : 0) <= expanded_slots) {
+        uint16_t *out = p.out + static_cast<int64_t>(part.group) * p.P * p.r;
+        if (!part.live()) {
+          uint32_t v[64];
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] = 0u;
+          write_result<OUT_T>(out, p.P, p.r, p0 + row, r0, v);
+        } else if (part.from_left()) {
+          if (t == 0) left_s = part;
+        } else {
+          if (part.to_right()) {
+            if (t == 0) right_s = part;
+          } else {
+            ok = mbar_wait_bounded(&acc_full[turn & 1], static_cast<uint32_t>(turn >> 1) & 1u, p.err, kErrTimeoutAcc,
+                                   20000000000ull);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tc_fence_after();
+            uint32_t v[64];
+            read_acc(tmem, static_cast<uint32_t>(turn & 1), quad, v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[turn & 1]);
+            write_result<OUT_T>(out, p.P, p.r, p0 + row, r0, v);
+          }
+          ++turn;
+        }
+        if (part.live()) done += part.e - part.b;
+        more = results.next(&part, true);
+      }
+    };
     if (ACT8) {
       // ---------------------------------------------------------- expand
-      // Thread t: row t / 2 of the step, 64-column half t % 2.
-      const int row = t >> 1, half = t & 1;
+      // Thread t: row t / 2 of the slot, 64-column half t % 2.
+      const int erow = t >> 1, half = t & 1;
       const int64_t kb = p.P / 64, cb = static_cast<int64_t>(p_tile) * 2 + half;
-      const uint32_t sw = static_cast<uint32_t>(row & 7);
-      const auto row_of = [&](int step) -> int64_t {
-        const int i = step * kStep + row;
-        return list ? __ldg(list + i) : (i < p.m ? i : -1);
+      const uint32_t sw = static_cast<uint32_t>(erow & 7);
+      const auto row_of = [&](int slot) -> int64_t {
+        if (slot < 0) return -1;
+        const int64_t i = static_cast<int64_t>(slot) * kSlot + erow;
+        return p.list ? __ldg(p.list + i) : (i < p.m ? i : -1);
       };
       const auto scale_of = [&](int64_t gr) -> uint32_t {
         return (gr >= 0 && cb < kb) ? static_cast<uint32_t>(__ldg(p.scale + gr * kb + cb)) * 0x10001u : 0u;
       };
-      // Row numbers two steps ahead, scales one step ahead.
-      int64_t row_nx = n_iters > 1 ? row_of(s_lo + 1) : -1;
-      uint32_t s_nx = n_iters > 0 ? scale_of(row_of(s_lo)) : 0u;
-      for (int li = 0; li < n_iters; ++li) {
+      // Row numbers two slots ahead, scales one slot ahead.
+      SlotWalk walk(p, lo, hi);
+      int slot = walk.next(), slot_nx = slot < 0 ? -1 : walk.next();
+      uint32_t s_nx = scale_of(row_of(slot));
+      int64_t row_nx = row_of(slot_nx);
+      for (int li = 0; slot >= 0; ++li) {
         const int s = li % kStages;
         const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
         const uint32_t s2 = s_nx;
-        if (li + 1 < n_iters) s_nx = scale_of(row_nx);
-        if (li + 2 < n_iters) row_nx = row_of(s_lo + li + 2);
-        if (!mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA)) { ok = false; break; }
+        s_nx = scale_of(row_nx);
+        slot = slot_nx;
+        slot_nx = slot < 0 ? -1 : walk.next();
+        row_nx = row_of(slot_nx);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA));
+        if (!ok) break;
         const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
-        const uint32_t code_row = l_s + kLBytes + kRBytes + static_cast<uint32_t>(row) * 128u;
-        const uint32_t out_row = l_s + static_cast<uint32_t>(half) * 8192u + static_cast<uint32_t>(row) * 128u;
+        const uint32_t code_row = l_s + kLBytes + kRBytes + static_cast<uint32_t>(erow) * 128u;
+        const uint32_t out_row = l_s + static_cast<uint32_t>(half) * 8192u + static_cast<uint32_t>(erow) * 128u;
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
           // 16 codes -> two 16-byte chunks; the halves walk them in an order
@@ -246,121 +454,116 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&expanded[s]);
+        // Results two slots late: their products have had time to finish.
+        flush(li - 1);
+        if (!ok) break;
       }
     }
-    // ------------------------------------------------------------ epilogue
-    // fp32 partial into the idle ring, along the output's contiguous dimension.
-    if (ok) ok = mbar_wait_bounded(&acc_bar, 0u, p.err, kErrTimeoutAcc, 20000000000ull);
-    if (ok) {
+    // ------------------------------------------------------------ results
+    if (ok) flush(0x7FFFFFFF);
+    // Partials of the groups that cross the share's borders, into the idle
+    // ring: every product of the share is done once the last accumulator is.
+    named_barrier_sync(1, 128);
+    const bool left = left_s.live(), right = right_s.live();
+    if (ok && right)
+      ok = mbar_wait_bounded(&acc_full[(turn - 1) & 1], static_cast<uint32_t>((turn - 1) >> 1) & 1u, p.err,
+                             kErrTimeoutAcc, 20000000000ull);
+    if (ok && left) ok = mbar_wait_bounded(&acc_full[kLeftAcc], 0u, p.err, kErrTimeoutAcc, 20000000000ull);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && (left || right)) {
       tc_fence_after();
-      const int quad = warp & 3;
-      const uint32_t row = static_cast<uint32_t>(quad * 32 + lane);
-#pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c0), v);
-        if (!OUT_T) {
-          const uint32_t dst = base + (row * kPartLd + static_cast<uint32_t>(c0)) * 4u;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = n_iters > 0 ? v[4 * j + e] : 0u;
-            sts128(dst + 16u * static_cast<uint32_t>(j), w);
-          }
-        } else {
-          const uint32_t dst = base + (static_cast<uint32_t>(c0) * 128u + row) * 4u;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float val = n_iters > 0 ? __uint_as_float(v[j]) : 0.f;
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(j) * 512u), "f"(val) : "memory");
-          }
-        }
+      uint32_t v[64];
+      if (left) {
+        read_acc(tmem, kLeftAcc, quad, v);
+        store_partial<OUT_T>(base, row, v);
+      }
+      if (right) {
+        read_acc(tmem, static_cast<uint32_t>((turn - 1) & 1), quad, v);
+        store_partial<OUT_T>(base + kPartBytes, row, v);
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
-  uint16_t *out = p.out + static_cast<int64_t>(group) * p.P * p.r;
-  split_reduce<64, kThreads, OUT_T>(base, kPartLd, out, OUT_T ? p.P : p.r, p.P, p.r, p0, r0, 1.0f);
-  cluster_sync_all();
+  if (nz > 1) {
+    cluster_sync_all();
+    // A crossing group is finished by all CTAs that hold a part of it, each
+    // an equal share of the tile in 16-byte pieces: the CTA where it starts
+    // holds its partial in the second buffer, the others in the first.
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const Part c = side == 0 ? left_s : right_s;
+      if (!c.live()) continue;
+      int zs = 0, ze = 0;
+      for (int i = 0; i < nz; ++i) {
+        if (share(i) <= c.s) zs = i;
+        if (share(i) <= c.s + c.slots() - 1) ze = i;
+      }
+      const int n = ze - zs + 1;
+      uint16_t *out = p.out + static_cast<int64_t>(c.group) * p.P * p.r;
+      const int hi_i = 2048 * (z - zs + 1) / n;
+      for (int i = 2048 * (z - zs) / n + static_cast<int>(threadIdx.x); i < hi_i; i += kThreads) {
+        // (row, 4 ranks) for a row-major result, (rank, 4 columns) transposed.
+        const uint32_t off = OUT_T ? static_cast<uint32_t>(i) * 16u
+                                   : (static_cast<uint32_t>(i / 16) * kPartLd + 4u * static_cast<uint32_t>(i % 16)) * 4u;
+        float4 part[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          part[q] = q < n ? ld_dsmem_v4(base + off + (q == 0 ? kPartBytes : 0u), static_cast<uint32_t>(zs + q))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc = part[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) {
+          if (q < n) {
+            acc.x += part[q].x;
+            acc.y += part[q].y;
+            acc.z += part[q].z;
+            acc.w += part[q].w;
+          }
+        }
+        const uint2 w = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        const int64_t pr = OUT_T ? p0 + 4 * (i % 32) : p0 + i / 16;
+        const int rr = OUT_T ? r0 + i / 32 : r0 + 4 * (i % 16);
+        if (pr >= p.P || rr >= p.r) continue;
+        *reinterpret_cast<uint2 *>(out + (OUT_T ? static_cast<int64_t>(rr) * p.P + pr : pr * p.r + rr)) = w;
+      }
+    }
+    cluster_sync_all();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(64u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
 }
 
-// The rows of each adapter, ascending, one CTA per adapter.  Adapter a's list
-// starts at entry 64 (floor(b / 64) + a), b the number of rows with a lower
-// id: such a list of c entries padded to a multiple of 64 ends before adapter
-// a + 1's starts, so no CTA needs another's count.  Warps take contiguous
-// runs of rows and count by ballots; no atomics, so the order is fixed.
-constexpr int kListThreads = 512;
-__global__ void __launch_bounds__(kListThreads) group_rows_kernel(const int32_t *__restrict__ ids, int m,
-                                                                  int32_t *__restrict__ start,
-                                                                  int32_t *__restrict__ count,
-                                                                  int32_t *__restrict__ list) {
-  __shared__ int eq_of[kListThreads / 32], lt_of[kListThreads / 32];
-  const int a = static_cast<int>(blockIdx.x);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kWarps = kListThreads / 32;
-  const int64_t run = ((static_cast<int64_t>(m) + 32 * kWarps - 1) / (32 * kWarps)) * 32;   // rows per warp
-  const int64_t lo = run * warp, hi = lo + run < m ? lo + run : m;
-  int eq = 0, lt = 0;
-#pragma unroll 4
-  for (int64_t i = lo; i < hi; i += 32) {
-    const int id = i + lane < hi ? __ldg(ids + i + lane) : -1;
-    eq += __popc(__ballot_sync(0xffffffffu, id == a));
-    lt += __popc(__ballot_sync(0xffffffffu, id >= 0 && id < a));
-  }
-  if (lane == 0) {
-    eq_of[warp] = eq;
-    lt_of[warp] = lt;
-  }
-  __syncthreads();
-  int before = 0, total = 0, lower = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += w < warp ? eq_of[w] : 0;
-    total += eq_of[w];
-    lower += lt_of[w];
-  }
-  const int64_t first = 64 * (static_cast<int64_t>(lower / 64) + a);
-  if (threadIdx.x == 0) {
-    start[a] = static_cast<int32_t>(first);
-    count[a] = total;
-  }
-  int32_t *dst = list + first;
-  const int padded = (total + 63) / 64 * 64;
-#pragma unroll 4
-  for (int64_t i = lo; i < hi; i += 32) {
-    const int id = i + lane < hi ? __ldg(ids + i + lane) : -1;
-    const unsigned hit = __ballot_sync(0xffffffffu, id == a);
-    if (id == a) {
-      const int at = before + __popc(hit & ((1u << lane) - 1u));
-      dst[at] = static_cast<int32_t>(i + lane);
-      // The last row also fills the padding.
-      if (at == total - 1)
-        for (int j = total; j < padded; ++j) dst[j] = static_cast<int32_t>(i + lane);
-    }
-    before += __popc(hit);
-  }
+// dA's tiles (transposed, L = X or its checkpoint), then dB's (L = dY): one
+// launch, so that neither product's last tiles leave the SMs idle.
+struct __align__(64) GradsParams {
+  GroupParams da, db;
+  int da_tiles;
+};
+template <bool ACT8>
+__global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_constant__ GradsParams p) {
+  const int tile = static_cast<int>(blockIdx.x);
+  if (tile < p.da_tiles)
+    group_tile<ACT8, true>(p.da, tile);
+  else
+    group_tile<false, false>(p.db, tile - p.da_tiles);
 }
 
-template <bool ACT8, bool OUT_T>
-cudaError_t launch(const GroupParams &p, int ptiles, int groups, int split, cudaStream_t stream) {
+template <bool ACT8>
+cudaError_t launch(const GradsParams &p, int tiles, int split, cudaStream_t stream) {
   static std::atomic<bool> configured[kMaxDevicesPerProcess] = {};
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(group_grads_kernel<ACT8, OUT_T>),
-                                static_cast<int>(smem_bytes<ACT8>()), configured);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(group_grads_kernel<ACT8>), static_cast<int>(kSmem),
+                                configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ptiles * p.rtiles), static_cast<unsigned>(groups), static_cast<unsigned>(split));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(split));
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<ACT8>();
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -369,71 +572,61 @@ cudaError_t launch(const GroupParams &p, int ptiles, int groups, int split, cuda
   attr[0].val.clusterDim.z = static_cast<unsigned>(split);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, group_grads_kernel<ACT8, OUT_T>, p);
+  e = cudaLaunchKernelEx(&cfg, group_grads_kernel<ACT8>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
-}  // namespace
-
-GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups) {
-  GroupRows g{};
-  int32_t *base = static_cast<int32_t *>(scratch);
-  g.groups = groups;
-  g.start = base;
-  g.count = base + groups;
-  g.list = base + (2 * static_cast<int64_t>(groups) + 63) / 64 * 64;
-  return g;
-}
-
-size_t group_rows_bytes(int64_t m, int32_t groups) {
-  const size_t head = (2 * static_cast<size_t>(groups) + 63) / 64 * 64;
-  return (head + 64 * (static_cast<size_t>(m) / 64 + static_cast<size_t>(groups))) * 4u;
-}
-
-cudaError_t launch_group_rows(const int32_t *ids, int64_t m, const GroupRows &g, cudaStream_t stream) {
-  group_rows_kernel<<<static_cast<unsigned>(g.groups), kListThreads, 0, stream>>>(ids, static_cast<int>(m), g.start,
-                                                                                  g.count, g.list);
-  count_launches(1);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_group_grads(const uint16_t *L, const Act8View *L8, int64_t m, int64_t P, const uint16_t *R,
-                               int32_t r, const GroupRows *g, uint16_t *out, bool transposed, cudaStream_t stream) {
-  GroupParams p{};
-  const int64_t cols = P;
+// The parameters of one product; null on failure.
+bool group_params(GroupParams *p, const uint16_t *L, const Act8View *L8, int64_t m, int64_t P, const uint16_t *R,
+                  int32_t r, const GroupRows *g, uint16_t *out) {
   if (L8) {
     const uint8_t *codes = reinterpret_cast<const uint8_t *>(L8->codes);
-    if (!encode_codes_map(&p.tmL, codes, m, cols, 128, kStep, true)) return cudaErrorInvalidValue;
-    if (!encode_codes_map(&p.tmLg, codes, m, cols, 128, 1, true)) return cudaErrorInvalidValue;
-    p.scale = L8->scale;
+    if (!encode_codes_map(&p->tmL, codes, m, P, 128, kSlot, true)) return false;
+    if (!encode_codes_map(&p->tmLg, codes, m, P, 128, 1, true)) return false;
+    p->scale = L8->scale;
   } else {
-    if (!encode_bf16_map(&p.tmL, L, m, cols, 64, kStep)) return cudaErrorInvalidValue;
-    if (!encode_bf16_map(&p.tmLg, L, m, cols, 64, 1)) return cudaErrorInvalidValue;
+    if (!encode_bf16_map(&p->tmL, L, m, P, 64, kSlot)) return false;
+    if (!encode_bf16_map(&p->tmLg, L, m, P, 64, 1)) return false;
   }
-  if (!encode_bf16_map(&p.tmR, R, m, r, 64, kStep)) return cudaErrorInvalidValue;
-  if (!encode_bf16_map(&p.tmRg, R, m, r, 64, 1)) return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p->tmR, R, m, r, 64, kSlot)) return false;
+  if (!encode_bf16_map(&p->tmRg, R, m, r, 64, 1)) return false;
   if (g) {
-    p.list = g->list;
-    p.start = g->start;
-    p.count = g->count;
+    p->list = g->list;
+    p->start = g->start;
+    p->count = g->count;
   }
-  p.out = out;
-  p.err = device_error_word();
-  p.P = P;
-  p.m = static_cast<int>(m);
-  p.r = r;
-  p.rtiles = (r + 63) / 64;
-  const int groups = g ? g->groups : 1;
-  const int ptiles = static_cast<int>((P + 127) / 128);
-  // At most min(groups, m) groups have rows; the split fills about two CTAs
-  // per SM with those.
-  const int64_t busy = groups < m ? groups : m;
-  const int steps = static_cast<int>((m + kStep - 1) / kStep);
-  const int split = choose_split(static_cast<int64_t>(ptiles) * p.rtiles * busy, steps);
-  if (L8) return launch<true, true>(p, ptiles, groups, split, stream);
-  return transposed ? launch<false, true>(p, ptiles, groups, split, stream)
-                    : launch<false, false>(p, ptiles, groups, split, stream);
+  p->out = out;
+  p->err = device_error_word();
+  p->P = P;
+  p->m = static_cast<int>(m);
+  p->r = r;
+  p->rtiles = (r + 63) / 64;
+  p->groups = g ? g->groups : 1;
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint16_t *U, int64_t k, uint16_t *dA,
+                               const uint16_t *dY, const uint16_t *T, int64_t n, uint16_t *dB, int64_t m, int32_t r,
+                               const GroupRows *g, cudaStream_t stream) {
+  GradsParams p{};
+  if (!group_params(&p.da, X, X8, m, k, U, r, g, dA)) return cudaErrorInvalidValue;
+  if (dB && !group_params(&p.db, dY, nullptr, m, n, T, r, g, dB)) return cudaErrorInvalidValue;
+  p.da_tiles = static_cast<int>((k + 127) / 128) * p.da.rtiles;
+  const int tiles = p.da_tiles + (dB ? static_cast<int>((n + 127) / 128) * p.db.rtiles : 0);
+  // At most m / 64 slots, and one more for every group with rows, two of
+  // them to a CTA at least; the largest clusters that all fit at once.
+  const int64_t busy = p.da.groups < m ? p.da.groups : m;
+  const int64_t slots = m / kSlot + busy;
+  static ClusterFit fit[2];
+  const void *kernel = X8 ? reinterpret_cast<const void *>(group_grads_kernel<true>)
+                          : reinterpret_cast<const void *>(group_grads_kernel<false>);
+  int clusters = 1;
+  const int split = fit[X8 ? 1 : 0].split(kernel, kThreads, kSmem, tiles, 2,
+                                          static_cast<int>(slots / 2 < 1 ? 1 : slots / 2 < 8 ? slots / 2 : 8), &clusters);
+  return X8 ? launch<true>(p, tiles, split, stream) : launch<false>(p, tiles, split, stream);
 }
 
 }  // namespace qlora

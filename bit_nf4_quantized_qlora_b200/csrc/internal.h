@@ -212,6 +212,18 @@ cudaError_t tc_tn_skinny(const uint16_t *Lt, int64_t mc, int64_t p, const uint16
 // tiles (tc_gemm.cu).
 int choose_split(int64_t tiles, int ksteps, int per_sm = 2);
 
+// How many clusters of 1 .. 8 CTAs of a kernel fit the device at once (asked
+// once per device and size: a cluster lies within one GPC, so the count is not
+// SMs / size).
+struct ClusterFit {
+  std::atomic<int> resident[kMaxDevicesPerProcess][9];
+  // The largest cluster size <= most_split of which `tiles` fit at once (1 if
+  // none does), with per_sm CTAs to an SM (the runtime counts one);
+  // *clusters is how many of that size do.
+  int split(const void *kernel, int threads, int smem_bytes, int64_t tiles, int per_sm, int most_split,
+            int *clusters);
+};
+
 // Many adapters on one weight -------------------------------------------------
 
 // The adapters of a call (device pointers): A [count x r x k], B [count x n x r],
@@ -223,7 +235,7 @@ struct AdapterView {
   int32_t count, r;
 };
 
-// Per row tile (128 rows when m <= 128, else 512) of a batch, in int32 words:
+// Per row tile (128 or 512 rows) of a batch, in int32 words:
 // [0] the number of adapters in the tile, [4 ..] their ids in order of first
 // appearance (`slots` entries), then per adapter rows/32 mask words whose bit
 // i is set for a row 32 w + i of that adapter.
@@ -232,14 +244,18 @@ struct TileLists {
   int64_t stride, tiles, bytes;
   int32_t slots, rows;
 };
-TileLists carve_tile_lists(void *scratch, int64_t m, int32_t count);
+TileLists carve_tile_lists(void *scratch, int64_t m, int32_t count, int32_t rows);
 size_t tile_lists_bytes(int64_t m, int32_t count);
+// The tile height of a product of m rows, `cols` output columns and `ksteps`
+// k-steps with many adapters.
+int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps);
 
 // out[m x r] = bf16(s_a . L . A_a^T) (L = X [m x k]) or, through_b,
 // bf16(s_a . L . B_a) (L = dY [m x n]); zeros in rows without an adapter.
-// Fills `lists` too unless null.  m > 0.
+// Fills `lists` and `rows` too unless null.  m > 0.
+struct GroupRows;
 cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
-                              uint16_t *out, const TileLists *lists, cudaStream_t stream);
+                              uint16_t *out, const TileLists *lists, const GroupRows *rows, cudaStream_t stream);
 // The first form for m <= 16 (no lists).
 cudaError_t launch_multi_proj_small(const uint16_t *X, int64_t m, int64_t k, const AdapterView &s, uint16_t *T,
                                     cudaStream_t stream);
@@ -260,7 +276,6 @@ struct GroupRows {
 };
 GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups);
 size_t group_rows_bytes(int64_t m, int32_t groups);
-cudaError_t launch_group_rows(const int32_t *ids, int64_t m, const GroupRows &g, cudaStream_t stream);
 
 // An 8-bit activation checkpoint: int8 codes [m x k], bf16 scales [m x k/64].
 struct Act8View {
@@ -268,11 +283,13 @@ struct Act8View {
   const uint16_t *scale;
 };
 
-// out_g = sum over group g's rows i of L[i, :]^T . R[i, :]  [P x r], or
-// transposed [r x P]; L bf16 [m x P], or its checkpoint L8 (transposed output
-// only); one group of all rows when g is null.  Every group is written.
-cudaError_t launch_group_grads(const uint16_t *L, const Act8View *L8, int64_t m, int64_t P, const uint16_t *R,
-                               int32_t r, const GroupRows *g, uint16_t *out, bool transposed, cudaStream_t stream);
+// dA_g = sum over group g's rows i of U[i, :]^T . X[i, :] [r x k], X bf16
+// [m x k] or its checkpoint X8, and (unless dB is null)
+// dB_g = sum of dY[i, :]^T . T[i, :] [n x r]; one group of all rows when g is
+// null.  Every group is written.
+cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint16_t *U, int64_t k, uint16_t *dA,
+                               const uint16_t *dY, const uint16_t *T, int64_t n, uint16_t *dB, int64_t m, int32_t r,
+                               const GroupRows *g, cudaStream_t stream);
 
 // 8-bit activation checkpoints (act8.cu); numel % 64 == 0.
 cudaError_t launch_act_quantize(const uint16_t *X, int64_t numel, int8_t *codes, uint16_t *scale, cudaStream_t stream);

@@ -7,10 +7,12 @@
 // lane i of the accumulator is row i of the tile), so the rank-r operand needs
 // no zero-filled copies and a row never meets another adapter's values.
 //
-// The rank dimension is cut into units of kUnit = 64, 32 or 16 columns (the
-// widest that divides r): a unit is one adapter's slice of that width, and
-// 64 / kUnit units share a 64-wide k-step.  A unit's K-major tile
-// [rows x kUnit] has rows of 128, 64 or 32 bytes under the swizzle of that
+// The rank dimension is cut into units of 64, 32 or 16 columns (the widest
+// that divides r): a unit is one adapter's slice of that width, and units that
+// lie in the same 64-column block of the rank share a 64-wide k-step.  The
+// rank-r operand (T or U) of a block is one [rows x 64] tile that stays in
+// shared memory for all of the block's steps.  A unit of a K-major adapter
+// matrix is a tile with rows of 128, 64 or 32 bytes under the swizzle of that
 // width, in atoms of 8 rows.
 #pragma once
 
@@ -83,19 +85,42 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// 16 bytes of global memory into shared memory, asynchronously (`bytes` = 0:
+// zeros), in the groups that cp_async_commit closes; cp_async_wait<N> leaves
+// the N youngest groups in flight.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 16 accumulator columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 
-// A call's tile lists and rank, as kernel parameters.
+// A call's tile lists and adapters, as kernel parameters.
 struct MultiParams {
   const int32_t *lists;
   int64_t stride;
   int32_t slots, rows;
   int32_t r, width;
+  const uint16_t *A, *B;    // [count x r x k], [count x n x r]
 };
 inline MultiParams multi_params(const AdapterView &ad, const TileLists &l) {
-  return MultiParams{l.base, l.stride, l.slots, l.rows, ad.r, unit_width(ad.r)};
+  return MultiParams{l.base, l.stride, l.slots, l.rows, ad.r, unit_width(ad.r), ad.A, ad.B};
 }
 
 // One tile's list.  Written by the kernel this one overlaps: read only after
@@ -105,51 +130,227 @@ struct MultiTile {
   const uint4 *mask;
   int adapters;
 };
-__device__ __forceinline__ MultiTile multi_tile(const MultiParams &p, int tile) {
-  const int32_t *t = p.lists + tile * p.stride;
-  return MultiTile{t + 4, reinterpret_cast<const uint4 *>(t + 4 + p.slots), __ldcg(t)};
+__device__ __forceinline__ const int32_t *multi_tile_at(const MultiParams &p, int tile) {
+  return p.lists + tile * p.stride;
+}
+__device__ __forceinline__ MultiTile multi_tile_of(const MultiParams &p, const int32_t *t, int adapters) {
+  return MultiTile{t + 4, reinterpret_cast<const uint4 *>(t + 4 + p.slots), adapters};
 }
 
-// A warp's window on the list: lane l holds entry `first` + l, so the latency
-// of a list read is paid once per 32 adapters.  Called by whole warps.
+// A warp's window on the list, so that the latency of a list read is paid once
+// per 32 adapters: entry first + i is in lane (i + 1) % 32.  Lane 0 runs the
+// main loop in the warps that issue copies and products; entries 0 .. 30 are
+// with the lanes that have been idle since the start.  Called by whole warps.
 struct AdapterWindow {
   int first = -32, id = 0;
+  __device__ __forceinline__ void prime(const MultiParams &p, const int32_t *t) {
+    first = 0;
+    const int i = (static_cast<int>(lane_id()) + 31) & 31;
+    id = i < p.slots && (i < 31 || p.slots > 31) ? __ldcg(t + 4 + i) : 0;
+  }
   __device__ __forceinline__ int at(const MultiTile &t, int slot) {
-    if (slot >= first + 32) {
+    if (slot < first || slot >= first + 32) {
       first = slot;
-      const int i = slot + static_cast<int>(lane_id());
+      const int i = slot + ((static_cast<int>(lane_id()) + 31) & 31);
       id = i < t.adapters ? __ldcg(t.list + i) : 0;
     }
-    return __shfl_sync(0xffffffffu, id, slot - first);
+    return __shfl_sync(0xffffffffu, id, (slot - first + 1) & 31);
   }
 };
-// Likewise the row masks of QUADS * 128 rows; off(q) is the lane mask of rows
+// Likewise the row masks of QUADS * 128 rows; off[q] is the lane mask of rows
 // 128 q .. of the tile: set where the row is not the adapter's.
 template <int QUADS>
 struct MaskWindow {
-  int first = -32;
+  int first = -32, current = -1;
   uint4 on[QUADS];
   uint4 off[QUADS];
+  __device__ __forceinline__ void prime(const MultiParams &p, const int32_t *t) {
+    first = 0;
+    const int i = (static_cast<int>(lane_id()) + 31) & 31;
+    const uint4 *mask = reinterpret_cast<const uint4 *>(t + 4 + p.slots);
+#pragma unroll
+    for (int q = 0; q < QUADS; ++q) on[q] = i < p.slots ? __ldcg(mask + i * QUADS + q) : make_uint4(0u, 0u, 0u, 0u);
+  }
   __device__ __forceinline__ void load(const MultiTile &t, int slot) {
-    if (slot >= first + 32) {
+    if (slot == current) return;
+    current = slot;
+    if (slot < first || slot >= first + 32) {
       first = slot;
-      const int i = slot + static_cast<int>(lane_id());
+      const int i = slot + ((static_cast<int>(lane_id()) + 31) & 31);
 #pragma unroll
       for (int q = 0; q < QUADS; ++q) on[q] = i < t.adapters ? __ldcg(t.mask + i * QUADS + q) : make_uint4(0u, 0u, 0u, 0u);
     }
-    const int l = slot - first;
+    const int l = (slot - first + 1) & 31;
 #pragma unroll
     for (int q = 0; q < QUADS; ++q)
       off[q] = make_uint4(~__shfl_sync(0xffffffffu, on[q].x, l), ~__shfl_sync(0xffffffffu, on[q].y, l),
                           ~__shfl_sync(0xffffffffu, on[q].z, l), ~__shfl_sync(0xffffffffu, on[q].w, l));
   }
 };
-// The adapter steps [lo, hi) of this CTA of a cluster along z.
-__device__ __forceinline__ void multi_share(int units, int per_step, int *lo, int *hi) {
-  const int steps = (units + per_step - 1) / per_step;
-  const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
-  *lo = static_cast<int>((static_cast<int64_t>(steps) * z) / nz);
-  *hi = static_cast<int>((static_cast<int64_t>(steps) * (z + 1)) / nz);
+
+// Opens a tile in a warp whose lane 0 arrives late: the other lanes read the
+// list as soon as its kernel is done and pass its adapters to `prefetch`.
+template <class Window, class Prefetch>
+__device__ __forceinline__ MultiTile multi_open(const MultiParams &p, int tile, Window &win, const Prefetch &prefetch) {
+  griddep_wait();
+  const int32_t *t = multi_tile_at(p, tile);
+  const int lane = static_cast<int>(lane_id());
+  int n = lane != 0 ? __ldcg(t) : 0;
+  win.prime(p, t);
+  if (lane != 0)
+    for (int i = lane - 1; i < n; i += 31) prefetch(__ldcg(t + 4 + i));
+  n = __shfl_sync(0xffffffffu, n, 1);
+  return multi_tile_of(p, t, n);
 }
+// `bytes` (a multiple of 16) at `src` into L2.
+__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+// An adapter's part of an output tile: rows [c0, c0 + cols) of B_a (forward),
+// or columns [c0, c0 + cols) of A_a's r rows.
+__device__ __forceinline__ void prefetch_adapter(const MultiParams &p, bool bwd, int64_t a, int64_t c0, int cols,
+                                                 int64_t out_cols) {
+  const int64_t left = out_cols - c0;
+  if (left <= 0) return;
+  const uint32_t c = static_cast<uint32_t>(left < cols ? left : cols);
+  if (!bwd) {
+    prefetch_l2(p.B + (a * out_cols + c0) * p.r, c * static_cast<uint32_t>(p.r) * 2u);
+  } else {
+    for (int j = 0; j < p.r; ++j) prefetch_l2(p.A + (a * p.r + j) * out_cols + c0, c * 2u);
+  }
+}
+
+// The adapter k-steps of a tile, block by block of the rank: every full
+// 64-column block has one step per adapter, the last partial block packs
+// 64 / width units into each.  A walk over them keeps its place in counters:
+// the warps that issue products have one instruction in flight at a time, and a
+// division would cost them as much as a step's products.
+struct MultiSteps {
+  int adapters, full, rest;            // full 64-column blocks; columns of the partial one
+  int lw;                              // log2 of the unit width
+  int per_step;                        // 64 / width
+  __device__ __forceinline__ MultiSteps(const MultiParams &p, const MultiTile &t)
+      : adapters(t.adapters), full(p.r >> 6), rest(p.r & 63), lw(p.width == 64 ? 6 : p.width == 32 ? 5 : 4),
+        per_step(64 >> lw) {}
+  __device__ __forceinline__ int count() const { return full * adapters + ((adapters * rest + 63) >> 6); }
+  // This CTA's share [lo, hi) along a cluster's z.
+  __device__ __forceinline__ void share(int *lo, int *hi) const {
+    const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
+    *lo = static_cast<int>((static_cast<int64_t>(count()) * z) / nz);
+    *hi = static_cast<int>((static_cast<int64_t>(count()) * (z + 1)) / nz);
+  }
+};
+struct MultiStep {
+  int block, units, per_adapter;          // rank block; units of the step, units of an adapter in the block
+  int slot, sub;                          // adapter and unit of the step's first
+  int left;                               // units of the block from this step on
+  int since;                              // steps of the walk in this block
+  // The step `st` of a walk that starts there.
+  __device__ __forceinline__ MultiStep(const MultiSteps &s, int st) {
+    const int in_full = s.full * s.adapters;
+    block = 0;
+    int at = st;
+    while (block < s.full && at >= s.adapters && s.adapters > 0) {
+      at -= s.adapters;
+      ++block;
+    }
+    if (st >= in_full) block = s.full;
+    open(s);
+    sub += at * s.per_step;
+    left -= sub;
+    slot = sub / per_adapter;
+    sub -= slot * per_adapter;
+    units = left < s.per_step ? left : s.per_step;
+  }
+  __device__ __forceinline__ void open(const MultiSteps &s) {
+    per_adapter = block < s.full ? s.per_step : (s.rest >> s.lw);
+    if (per_adapter == 0) per_adapter = 1;       // past the last block
+    left = s.adapters * per_adapter;
+    slot = sub = since = 0;
+    units = left < s.per_step ? left : s.per_step;
+  }
+  // To the walk's next step.
+  __device__ __forceinline__ void next(const MultiSteps &s) {
+    left -= units;
+    ++since;
+    if (left == 0) {
+      ++block;
+      open(s);
+      return;
+    }
+    sub += units;
+    while (sub >= per_adapter) {
+      sub -= per_adapter;
+      ++slot;
+    }
+    units = left < s.per_step ? left : s.per_step;
+  }
+  // To the step's next unit (of a copy).
+  __device__ __forceinline__ void advance() {
+    if (++sub == per_adapter) {
+      sub = 0;
+      ++slot;
+    }
+  }
+};
+
+// A thread's part of a step's K-major adapter tile [ROWS x 64], ROWS threads:
+// 8 pieces of 16 bytes, taken from the matrices B_a [n x r] of the step's
+// adapters and stored as 64 / w units of ROWS rows under the unit's swizzle.
+// Plain loads, consecutive lanes on consecutive bytes: a unit row of 32 or 64
+// bytes would cost the copy engine as much as one of 128 (bulk copies of whole
+// adapters put in order in shared memory, and boxes for the 128-byte rows, took
+// the same time).
+template <int ROWS>
+struct MultiRows {
+  uint4 v[8];
+  template <int W, class Window>
+  __device__ __forceinline__ void load_w(const MultiParams &p, MultiStep s, Window &win, const MultiTile &t, int64_t n,
+                                         int64_t n0, int thread) {
+    constexpr int kPieces = W / 8;      // of a unit row
+#pragma unroll
+    for (int u = 0; u < 64 / W; ++u) {
+      const int a = u < s.units ? win.at(t, s.slot) : 0;
+      const uint16_t *src = p.B + (a * n + n0) * p.r + s.block * 64 + s.sub * W;
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const int j = c * ROWS + thread, row = j / kPieces;
+        v[u * kPieces + c] = u < s.units && n0 + row < n
+                                 ? __ldg(reinterpret_cast<const uint4 *>(src + row * p.r) + j % kPieces)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+      }
+      s.advance();
+    }
+  }
+  template <class Window>
+  __device__ __forceinline__ void load(const MultiParams &p, const MultiStep &s, Window &win, const MultiTile &t,
+                                       int64_t n, int64_t n0, int thread) {
+    if (p.width == 16)
+      load_w<16>(p, s, win, t, n, n0, thread);
+    else if (p.width == 32)
+      load_w<32>(p, s, win, t, n, n0, thread);
+    else
+      load_w<64>(p, s, win, t, n, n0, thread);
+  }
+  template <int W>
+  __device__ __forceinline__ void store_w(uint32_t tile, int thread) const {
+    constexpr int kPieces = W / 8;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int j = (q % kPieces) * ROWS + thread, row = j / kPieces;
+      const int sw = (row >> (W == 64 ? 0 : W == 32 ? 1 : 2)) & (kPieces - 1);
+      const uint32_t o[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+      sts128(tile + static_cast<uint32_t>(((q / kPieces) * ROWS + row) * W * 2 + (((j % kPieces) ^ sw) << 4)), o);
+    }
+  }
+  __device__ __forceinline__ void store(const MultiParams &p, uint32_t tile, int thread) const {
+    if (p.width == 16)
+      store_w<16>(tile, thread);
+    else if (p.width == 32)
+      store_w<32>(tile, thread);
+    else
+      store_w<64>(tile, thread);
+  }
+};
 
 }  // namespace qlora

@@ -10,14 +10,19 @@
 //
 // tcgen05 path (multi_proj_kernel).  A CTA takes 128 rows of the batch, lists
 // the adapters that occur in them (in order of first appearance) and packs
-// their rank columns into the N dimension of one product: 64 / w units of w
-// columns each (w = 64, 32 or 16, the widest that divides r).  The
-// accumulator then holds every row against every listed adapter; a row keeps
-// only its own adapter's columns.  So rows in any order need no sorting, a
-// batch ordered by adapter costs one pass per tile, and the rows of X are read
-// once per 64 rank columns present.  Passes are spread over CTAs, K over a
-// cluster of up to 8 CTAs whose fp32 partials are added in rank order.
-// Bound by reading X and the adapters present (HBM / L2).
+// their rank columns side by side into the N dimension of one product, up to
+// 256 columns a pass, in units of w columns (w = 64, 32 or 16, the widest that
+// divides r).  The accumulator then holds every row against every adapter of
+// the pass; a row keeps only its own adapter's columns.  So rows in any order
+// need no sorting, a batch ordered by adapter takes one pass per tile, and X is
+// read once per 256 rank columns present.  K is split over a cluster of up to
+// 8 CTAs whose fp32 partials (each row's own r columns) are added in rank
+// order; narrower passes on more CTAs when the tiles alone leave SMs idle.
+// Bound by reading X and the adapters present (HBM / L2).  The copy engine
+// takes as long for a box row of 32 or 64 bytes as for one of 128 bytes, so in
+// U's form with w < 64 the epilogue warps fetch the adapter tiles with 16-byte
+// asynchronous copies.  (Two warps issuing alternate k-steps into accumulators
+// of their own took the same time: the copies set the pace.)
 //
 // Decode path (multi_proj_small_kernel, m <= 16): a CTA per (adapter row,
 // token), a plain dot product: the tokens' adapters are mostly distinct, so
@@ -25,8 +30,8 @@
 //
 // Tile lists.  The kernels that add T . B^T (or U . A) to a tile need its
 // adapters and, for each, which rows use it (the lane masks of the masked
-// products).  One extra CTA per 512-row tile (128 rows when m <= 128) writes
-// them beside the projection, at no extra launch.
+// products), and the adapter gradients each adapter's rows.  Two more warps
+// of the projection write them beside it, at no extra launch.
 #include <cuda.h>
 
 #include "internal.h"
@@ -38,30 +43,40 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kRows = 128;
-constexpr int kStages = 4;
-constexpr int kThreads = 192;                     // TMA warp, MMA warp, four epilogue warps
+constexpr int kMaxStages = 8;
+constexpr int kMaxCols = 256;                     // rank columns of a pass
+constexpr int kListThreads = 64;
+// TMA warp, MMA warp, four adapter-tile / epilogue warps, two list warps.
+constexpr int kThreads = 192 + kListThreads;
 constexpr uint32_t kABytes = 128u * kBK * 2u;     // 16 KB
-constexpr uint32_t kBBytes = 64u * kBK * 2u;      // 8 KB
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024u;
-constexpr uint32_t kPartLd = 64u + 4u;
-static_assert(2u * (kSmemBytes + 4096u) <= 227u * 1024u, "two CTAs per SM");
-static_assert(kStages * kStageBytes >= 128u * kPartLd * 4u, "room for the fp32 partial tile");
-// The list builder's arrays: ids, first occurrence and slot of 512 rows, then
-// 16 mask words for each of up to 512 adapters.
-static_assert(kStages * kStageBytes >= 3u * 2048u + 512u * 64u, "room for the tile lists");
+constexpr uint32_t kColBytes = kBK * 2u;          // shared memory of one rank column of a k-step
+constexpr uint32_t kRing = 200u * 1024u;
+constexpr uint32_t kSmemBytes = kRing + 1024u;
+// The ring holds X's 16 KB tiles first, then the adapter tiles: 8 stages at 64
+// columns, 4 at 256.
+constexpr uint32_t kMinStages = 4;
+static_assert(kRing / (kABytes + kMaxCols * kColBytes) >= kMinStages, "four stages at the widest");
+static_assert(kRing >= 128u * (kMaxCols + 4u) * 4u, "room for the fp32 partial tile");
+constexpr int64_t kRowsInside = 8192;             // batches whose row lists the list warps make
+constexpr int kAhead = 3;                         // k-steps of adapter copies in flight per thread
+static_assert(kRing / (kABytes + kMaxCols * kColBytes) > kAhead, "a stage is refilled after its copies were reported");
 
 struct __align__(64) ProjParams {
-  CUtensorMap tmL;        // X or dY [m x kc], box {64, 128}
-  CUtensorMap tmR;        // A {kc, r, count} box {64, w, 1}; B {r, kc, count} box {w, 64, 1}
+  CUtensorMap tmL;        // X or dY [m x kc], box {64, tile_rows}
+  CUtensorMap tmR;        // A {kc, r, count} box {64, w, 1}; B {r, kc, count} box {64, 64, 1} (w = 64)
+  const uint16_t *R;      // B [count x kc x r] (w < 64)
+  int64_t kc;
   const int32_t *ids;
   const float *scale;
   uint16_t *out;          // [m x r]
   unsigned *err;
+  GroupRows rows;         // row lists (null list: not wanted)
   int32_t *lists;         // tile lists (null: not wanted)
   int64_t list_stride;    // int32 per tile
-  int list_slots, list_rows, list_tiles;
+  int list_slots, list_rows;
   int m, r, count, width, nk, pass_ctas;
+  int per_pass;           // adapters of a pass
+  int tile_rows;          // 128, or 64 where that fills the SMs better
 };
 
 __device__ __forceinline__ int row_id(const ProjParams &p, int64_t row) {
@@ -69,234 +84,404 @@ __device__ __forceinline__ int row_id(const ProjParams &p, int64_t row) {
   return id >= 0 && id < p.count ? id : -1;
 }
 
-// One tile's adapters and row masks (layout: see TileLists).
-__device__ void build_lists(const ProjParams &p, int tile, uint8_t *smem) {
-  const int n = p.list_rows, words = n / 32;
-  int *ids = reinterpret_cast<int *>(smem), *first = ids + 512, *slot = first + 512;
-  uint32_t *mask = reinterpret_cast<uint32_t *>(slot + 512);
-  __shared__ int total_s;
-  for (int i = threadIdx.x; i < n; i += kThreads) ids[i] = row_id(p, static_cast<int64_t>(tile) * n + i);
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int id = ids[i];
-    int j = 0;
-    while (ids[j] != id) ++j;
-    first[i] = j;
+// Finds or adds `id` in a table of SIZE keys (empty: -1) and notes `row` as a
+// row of it: first[place] ends as the lowest row.  Returns the place.
+template <int SIZE>
+__device__ __forceinline__ int table_add(int *key, int *first, int id, int row) {
+  uint32_t h = (static_cast<uint32_t>(id) * 2654435761u) >> 16 & (SIZE - 1);
+  for (;;) {     // ends: fewer ids than places
+    const int old = atomicCAS(&key[h], -1, id);
+    if (old == -1 || old == id) break;
+    h = (h + 1) & (SIZE - 1);
   }
-  __syncthreads();
+  atomicMin(&first[h], row);
+  return static_cast<int>(h);
+}
+
+// The list warps' arrays: ids, table place and slot of up to 512 rows, and the
+// table (key, first row).
+struct ListSmem {
+  int id[512], place[512], slot[512], key[1024], first[1024];
+};
+
+// One tile's adapters and row masks (layout: see TileLists), by thread t of
+// the list warps (named barrier 1).
+__device__ void build_lists(const ProjParams &p, int tile, ListSmem &s, int t) {
+  const int n = p.list_rows, words = n / 32, lane = t & 31;
+  for (int i = t; i < 1024; i += kListThreads) {
+    s.key[i] = -1;
+    s.first[i] = 0x7FFFFFFF;
+  }
+  for (int i = t; i < n; i += kListThreads) s.id[i] = row_id(p, static_cast<int64_t>(tile) * n + i);
+  named_barrier_sync(1, kListThreads);
+  for (int i = t; i < n; i += kListThreads)
+    if (s.id[i] >= 0) s.place[i] = table_add<1024>(s.key, s.first, s.id[i], i);
+  named_barrier_sync(1, kListThreads);
   int32_t *out = p.lists + tile * p.list_stride;
-  if (threadIdx.x < 32) {
-    int base = 0;
-    for (int c = 0; c < words; ++c) {
-      const int i = 32 * c + static_cast<int>(threadIdx.x);
-      const bool lead = ids[i] >= 0 && first[i] == i;
-      const unsigned b = __ballot_sync(0xffffffffu, lead);
-      const int s = base + __popc(b & ((1u << threadIdx.x) - 1u));
-      if (lead) {
-        slot[i] = s;
-        out[4 + s] = ids[i];
-      }
-      base += __popc(b);
+  uint32_t *mask = reinterpret_cast<uint32_t *>(out + 4 + p.list_slots);
+  // Both warps number the leaders; each stores half of the entries.
+  int total = 0;
+  for (int c = 0; c < words; ++c) {
+    const int i = 32 * c + lane;
+    const bool lead = s.id[i] >= 0 && s.first[s.place[i]] == i;
+    const unsigned b = __ballot_sync(0xffffffffu, lead);
+    const int at = total + __popc(b & ((1u << lane) - 1u));
+    if (lead && (c & 1) == (t >> 5)) {
+      s.slot[i] = at;
+      out[4 + at] = s.id[i];
     }
-    if (threadIdx.x == 0) {
-      out[0] = base;
-      total_s = base;
-    }
+    total += __popc(b);
   }
-  __syncthreads();
-  const int total = total_s;
-  for (int i = threadIdx.x; i < total * words; i += kThreads) mask[i] = 0u;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    if (ids[i] >= 0) atomicOr(&mask[slot[first[i]] * words + (i >> 5)], 1u << (i & 31));
-  __syncthreads();
-  uint32_t *gmask = reinterpret_cast<uint32_t *>(out + 4 + p.list_slots);
-  for (int i = threadIdx.x; i < total * words; i += kThreads) gmask[i] = mask[i];
+  if (t == 0) out[0] = total;
+  for (int i = t; i < total * words; i += kListThreads) mask[i] = 0u;
+  named_barrier_sync(1, kListThreads);
+  // A mask word per (adapter, 32 rows) that has a row, from the lanes that
+  // hold the same id.
+  for (int c = t >> 5; c < words; c += 2) {
+    const int i = 32 * c + lane, id = s.id[i];
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0u) mask[s.slot[s.first[s.place[i]]] * words + c] = same;
+  }
+}
+
+// The rows of adapter a in ascending order (layout: see GroupRows), by thread
+// t of `threads`, whose warps take contiguous runs of rows and count by
+// ballots: no atomics, so the order is fixed.  Adapter a's list starts at entry
+// 64 (floor(b / 64) + a), b the number of rows with a lower id: such a list of
+// c entries padded to a multiple of 64 ends before adapter a + 1's starts, so
+// nobody needs another adapter's count.
+template <int THREADS, class Sync>
+__device__ void list_rows(const int32_t *ids, int m, int a, const GroupRows &g, int (*count_of)[2], int t,
+                          const Sync &sync) {
+  constexpr int kWarps = THREADS / 32;
+  const int warp = t >> 5, lane = t & 31;
+  const int64_t run = ((static_cast<int64_t>(m) + 32 * kWarps - 1) / (32 * kWarps)) * 32;   // rows per warp
+  const int64_t lo = run * warp, hi = lo + run < m ? lo + run : m;
+  int eq = 0, lt = 0;
+#pragma unroll 4
+  for (int64_t i = lo; i < hi; i += 32) {
+    const int id = i + lane < hi ? __ldg(ids + i + lane) : -1;
+    eq += __popc(__ballot_sync(0xffffffffu, id == a));
+    lt += __popc(__ballot_sync(0xffffffffu, id >= 0 && id < a));
+  }
+  if (lane == 0) {
+    count_of[warp][0] = eq;
+    count_of[warp][1] = lt;
+  }
+  sync();
+  int before = 0, total = 0, lower = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? count_of[w][0] : 0;
+    total += count_of[w][0];
+    lower += count_of[w][1];
+  }
+  const int64_t first = 64 * (static_cast<int64_t>(lower / 64) + a);
+  if (t == 0) {
+    g.start[a] = static_cast<int32_t>(first);
+    g.count[a] = total;
+  }
+  int32_t *dst = g.list + first;
+  const int padded = (total + 63) / 64 * 64;
+#pragma unroll 4
+  for (int64_t i = lo; i < hi; i += 32) {
+    const int id = i + lane < hi ? __ldg(ids + i + lane) : -1;
+    const unsigned hit = __ballot_sync(0xffffffffu, id == a);
+    if (id == a) {
+      const int at = before + __popc(hit & ((1u << lane) - 1u));
+      dst[at] = static_cast<int32_t>(i + lane);
+      // The last row also fills the padding.
+      if (at == total - 1)
+        for (int j = total; j < padded; ++j) dst[j] = static_cast<int32_t>(i + lane);
+    }
+    before += __popc(hit);
+  }
+  sync();
+}
+
+// The lists of a long batch, one CTA per adapter (a short batch's are made by
+// the projection's list warps).
+constexpr int kRowsThreads = 512;
+__global__ void __launch_bounds__(kRowsThreads) group_rows_kernel(const int32_t *__restrict__ ids, int m, GroupRows g) {
+  __shared__ int count_of[kRowsThreads / 32][2];
+  list_rows<kRowsThreads>(ids, m, static_cast<int>(blockIdx.x), g, count_of, static_cast<int>(threadIdx.x),
+                          [] { __syncthreads(); });
 }
 
 // R_MN: R is [count x kc x r] (MN-major operand); else [count x r x kc].
 template <bool R_MN>
-__global__ void __launch_bounds__(kThreads, 2) multi_proj_kernel(const __grid_constant__ ProjParams p) {
+__global__ void __launch_bounds__(kThreads, 1) multi_proj_kernel(const __grid_constant__ ProjParams p) {
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
   __shared__ __align__(8) uint64_t acc_bar;
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) int ids[kRows];
-  __shared__ int list[kRows], slot_of[kRows], lead_count[4];
+  __shared__ int2 unit_list[kMaxCols / 16];
+  __shared__ int key[256], first[256], list[kRows], slot_of[kRows], lead_slot[kRows], lead_count[4];
+
+  __shared__ ListSmem lists_s;
+  __shared__ int failed, rows_count[kListThreads / 32][2];
 
   // The kernel that consumes the output may start now; it waits for this
   // grid before it reads the output or the lists.
   griddep_launch();
-  const uint32_t raw = smem_u32(dsmem);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
   const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
-  if (static_cast<int>(blockIdx.x) == p.pass_ctas) {
-    if (z == 0 && static_cast<int>(blockIdx.y) < p.list_tiles)
-      build_lists(p, static_cast<int>(blockIdx.y), dsmem + (base - raw));
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m_tile = static_cast<int>(blockIdx.y);
   const int k_lo = static_cast<int>((static_cast<int64_t>(p.nk) * z) / nz);
   const int k_hi = static_cast<int>((static_cast<int64_t>(p.nk) * (z + 1)) / nz);
+  const int steps = k_hi - k_lo;
+  const bool loaders = R_MN && p.width < 64;      // adapter tiles by the epilogue warps
+  // X's copy for step j of a pass into stage s.  64-row tiles leave the second
+  // half of A as it is: its accumulator rows are never read.
+  const auto load_x = [&](int s, int j) {
+    tma_load_2d(base + static_cast<uint32_t>(s) * kABytes, &p.tmL, &full[s], (k_lo + j) * kBK,
+                m_tile * p.tile_rows);
+  };
+  int issued = 0;               // k-steps whose copies were issued (producer)
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], loaders ? 1 + 4 : 1);     // the copies, and the adapter-tile warps
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_bar, 1);
+    failed = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    // The first pass's copies of X start before the adapters are listed (their
+    // bytes are announced with the adapters').
+    if (blockIdx.x == 0)
+      for (; issued < static_cast<int>(kMinStages) && issued < steps; ++issued) load_x(issued, issued);
+  }
+  // The tile's adapters: a row leads if it is its id's first; leaders are
+  // numbered in row order.
+  const int t = static_cast<int>(threadIdx.x) - 64;
+  const bool row_warp = warp >= 2 && warp < 6;
+  const int my_id = row_warp && t < p.tile_rows ? row_id(p, static_cast<int64_t>(m_tile) * p.tile_rows + t) : -1;
+  for (int i = threadIdx.x; i < 256; i += kThreads) {
+    key[i] = -1;
+    first[i] = 0x7FFFFFFF;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                 "r"(64u)
+                 "r"(static_cast<uint32_t>(kMaxCols))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // The tile's adapters: a row leads if no earlier row has its id; leaders
-  // are numbered in row order.
-  const int t = static_cast<int>(threadIdx.x) - 64;
-  const int my_id = t >= 0 ? row_id(p, static_cast<int64_t>(m_tile) * kRows + t) : -1;
-  if (t >= 0) ids[t] = my_id;
   __syncthreads();
-  int first = t;
-  unsigned lead_bits = 0u;
-  if (t >= 0) {
-    for (int j = 0; j < t; j += 4) {
-      const int4 v = *reinterpret_cast<const int4 *>(ids + j);
-      const int at = v.x == my_id ? j : v.y == my_id ? j + 1 : v.z == my_id ? j + 2 : v.w == my_id ? j + 3 : t;
-      if (at < t) {
-        first = at;
-        break;
-      }
-    }
-    lead_bits = __ballot_sync(0xffffffffu, my_id >= 0 && first == t);
-    if (lane == 0) lead_count[t >> 5] = __popc(lead_bits);
-  }
+  const int place = my_id >= 0 ? table_add<256>(key, first, my_id, t) : -1;
   __syncthreads();
-  const int listed = lead_count[0] + lead_count[1] + lead_count[2] + lead_count[3];
-  if (t >= 0 && my_id >= 0 && first == t) {
+  const bool lead = my_id >= 0 && first[place] == t;
+  const unsigned lead_bits = __ballot_sync(0xffffffffu, lead);
+  if (row_warp && lane == 0) lead_count[t >> 5] = __popc(lead_bits);
+  __syncthreads();
+  if (lead) {
     int s = __popc(lead_bits & ((1u << lane) - 1u));
     for (int w = 0; w < (t >> 5); ++w) s += lead_count[w];
     list[s] = my_id;
-    slot_of[t] = s;
+    lead_slot[t] = s;
   }
   __syncthreads();
-  // Read by everyone before a non-leader overwrites its own entry.
-  const int my_slot = t >= 0 && my_id >= 0 ? slot_of[first] : -1;
-  __syncthreads();
-  if (t >= 0) slot_of[t] = my_slot;
+  const int listed = lead_count[0] + lead_count[1] + lead_count[2] + lead_count[3];
+  const int my_slot = my_id >= 0 ? lead_slot[first[place]] : -1;
+  if (row_warp) slot_of[t] = my_slot;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  const int w = p.width, per_adapter = p.r / w, per_pass = 64 / w;
-  const int units = listed * per_adapter;
-  const int passes = (units + per_pass - 1) / per_pass;
-  const uint32_t unit_bytes = static_cast<uint32_t>(w) * 128u;
-  int step = 0;         // k-steps of the CTA's earlier passes (ring position)
-  int issued = 0;       // k-steps whose copies were issued (producer)
+  const int w = p.width, per_adapter = p.r / w;
+  const int passes = (listed + p.per_pass - 1) / p.per_pass;
+  const uint32_t unit_bytes = static_cast<uint32_t>(w) * kColBytes;
+  const int widest = listed < p.per_pass ? listed : p.per_pass;
+  const uint32_t b_bytes = static_cast<uint32_t>(widest * p.r) * kColBytes;
+  const int stages = kRing / (kABytes + b_bytes) < kMaxStages ? static_cast<int>(kRing / (kABytes + b_bytes)) : kMaxStages;
+  const uint32_t b_ring = base + static_cast<uint32_t>(stages) * kABytes;
+  const uint32_t part_ld = static_cast<uint32_t>(p.r) + 4u;
+  int ring = 0;                 // stage and parity of the next k-step (producer, MMA)
+  uint32_t parity = 0u;
   bool ok = true;
   uint32_t acc_phase = 0u;
 
+  if (warp >= 6 && p.lists && blockIdx.x == 0 && z == 0 && (m_tile * p.tile_rows) % p.list_rows == 0)
+    build_lists(p, m_tile * p.tile_rows / p.list_rows, lists_s, static_cast<int>(threadIdx.x) - 192);
+  if (warp >= 6 && p.rows.list) {
+    // From the last CTA on: the first ones make the tile lists.
+    const int ctas = static_cast<int>(gridDim.x * gridDim.y * gridDim.z);
+    const int cta = ctas - 1 - static_cast<int>((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x);
+    for (int a = cta; a < p.count; a += ctas)
+      list_rows<kListThreads>(p.ids, p.m, a, p.rows, rows_count, static_cast<int>(threadIdx.x) - 192,
+                              [] { named_barrier_sync(1, kListThreads); });
+  }
+
   for (int pass = static_cast<int>(blockIdx.x); pass < passes; pass += p.pass_ctas) {
-    const int u0 = pass * per_pass;
-    const int nu = units - u0 < per_pass ? units - u0 : per_pass;
-    const int steps = k_hi - k_lo;
+    const int a0 = pass * p.per_pass;                                       // the pass's adapters
+    const int na = listed - a0 < p.per_pass ? listed - a0 : p.per_pass;
+    const int nu = na * per_adapter;
+    // The pass's units: adapter and first rank column.
+    if (warp < 6) {
+      for (int u = threadIdx.x; u < nu; u += 192)
+        unit_list[u] = make_int2(list[a0 + u / per_adapter], (u % per_adapter) * w);
+      named_barrier_sync(2, kThreads - kListThreads);
+    }
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       if (lane == 0 && ok) {
-        for (int j = 0; j < steps && ok; ++j) {
-          const int s = (step + j) % kStages;
-          const uint32_t ph = static_cast<uint32_t>((step + j) / kStages) & 1u;
-          ok = mbar_wait_bounded(&empty[s], ph ^ 1u, p.err, kErrTimeoutEmpty);
+        for (int j = 0; j < steps; ++j) {
+          // The first pass's first copies of X are under way.
+          const bool fresh = pass != static_cast<int>(blockIdx.x) || j >= issued;
+          ok = mbar_wait_bounded(&empty[ring], parity ^ 1u, p.err, kErrTimeoutEmpty);
           if (!ok) break;
-          const uint32_t a_s = base + static_cast<uint32_t>(s) * kStageBytes, b_s = a_s + kABytes;
-          mbar_arrive_expect_tx(&full[s], kABytes + static_cast<uint32_t>(nu) * unit_bytes);
-          const int kx = (k_lo + j) * kBK;
-          tma_load_2d(a_s, &p.tmL, &full[s], kx, m_tile * kRows);
-          for (int u = 0; u < nu; ++u) {
-            const int a = list[(u0 + u) / per_adapter], c = (u0 + u) % per_adapter;
-            const uint32_t dst = b_s + static_cast<uint32_t>(u) * unit_bytes;
-            if (R_MN)
-              tma_load_3d(dst, &p.tmR, &full[s], c * w, kx, a);
-            else
-              tma_load_3d(dst, &p.tmR, &full[s], kx, c * w, a);
+          mbar_arrive_expect_tx(&full[ring], static_cast<uint32_t>(p.tile_rows) * 128u +
+                                                 (loaders ? 0u : static_cast<uint32_t>(nu) * unit_bytes));
+          if (fresh) {
+            load_x(ring, j);
+            ++issued;
           }
-          ++issued;
+          if (!loaders) {
+            const uint32_t b_s = b_ring + static_cast<uint32_t>(ring) * b_bytes;
+            for (int u = 0; u < nu; ++u) {
+              const int2 unit = unit_list[u];
+              if (R_MN)
+                tma_load_3d(b_s + static_cast<uint32_t>(u) * unit_bytes, &p.tmR, &full[ring], unit.y, (k_lo + j) * kBK,
+                            unit.x);
+              else
+                tma_load_3d(b_s + static_cast<uint32_t>(u) * unit_bytes, &p.tmR, &full[ring], (k_lo + j) * kBK, unit.y,
+                            unit.x);
+            }
+          }
+          if (++ring == stages) {
+            ring = 0;
+            parity ^= 1u;
+          }
         }
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0 && ok) {
+        // One thread issues everything, so what a step does not change is
+        // kept in registers: descriptors advance by additions (16-byte units).
         const uint32_t idesc = make_idesc(nu * w, false, R_MN);
-        for (int j = 0; j < steps && ok; ++j) {
-          const int s = (step + j) % kStages;
-          const uint32_t ph = static_cast<uint32_t>((step + j) / kStages) & 1u;
-          ok = mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA);
+        const uint64_t ad0 = smem_desc(base, 16u, 1024u);
+        // MN-major units: [64 k-rows x w columns], one behind the other.
+        const uint64_t bd0 = R_MN ? smem_desc_unit(b_ring, unit_bytes, static_cast<uint32_t>(16 * w), w)
+                                  : smem_desc(b_ring, 16u, 1024u);
+        const uint32_t b_step = R_MN ? static_cast<uint32_t>(2 * w) : 2u;
+        for (int j = 0; j < steps; ++j) {
+          ok = mbar_wait_bounded(&full[ring], parity, p.err, kErrTimeoutFullA);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_s = base + static_cast<uint32_t>(s) * kStageBytes, b_s = a_s + kABytes;
+          uint64_t ad = ad0 + static_cast<uint32_t>(ring) * (kABytes >> 4);
+          uint64_t bd = bd0 + static_cast<uint32_t>(ring) * (b_bytes >> 4);
+          umma_f16(tmem, ad, bd, idesc, j > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            // MN-major units: [64 k-rows x w columns], one behind the other.
-            const uint64_t bd = R_MN ? smem_desc_unit(b_s + static_cast<uint32_t>(kk * 32 * w), unit_bytes,
-                                                      static_cast<uint32_t>(16 * w), w)
-                                     : smem_desc(b_s + kk * 32u, 16u, 1024u);
-            umma_f16(tmem, smem_desc(a_s + kk * 32u, 16u, 1024u), bd, idesc, (j > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 1; kk < kBK / 16; ++kk) {
+            ad += 2u;
+            bd += b_step;
+            umma_f16(tmem, ad, bd, idesc, 1u);
           }
-          umma_commit(&empty[s]);
+          umma_commit(&empty[ring]);
+          if (++ring == stages) {
+            ring = 0;
+            parity ^= 1u;
+          }
         }
         if (ok) umma_commit(&acc_bar);
       }
-    } else {
+    } else if (row_warp) {
+      // ---------------------------------------------------------- adapter tiles
+      if (loaders) {
+        // Each thread's 16-byte pieces of the k-step: 128 threads take
+        // consecutive pieces of the pass's units, [64 k-rows x w columns] with
+        // rows of 2w bytes.
+        int done_ring = ring;                 // stage whose copies are waited for next
+        const int pieces = nu * w * 8 / 128;
+        const int lw = w == 32 ? 5 : 4;
+        for (int j = 0; j < steps + kAhead && ok; ++j) {
+          if (j < steps) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[ring], parity ^ 1u, p.err, kErrTimeoutEmpty));
+            if (!ok) break;
+            const uint32_t b_s = b_ring + static_cast<uint32_t>(ring) * b_bytes;
+            const int64_t kx = static_cast<int64_t>(k_lo + j) * kBK;
+            for (int q = 0; q < pieces; ++q) {
+              const int i = q * 128 + t;
+              const int u = i >> (lw + 3), rem = i & (8 * w - 1), row = rem >> (lw - 3), c = rem & (w / 8 - 1);
+              const int sw = (row >> (lw == 5 ? 1 : 2)) & (w / 8 - 1);
+              const int2 unit = unit_list[u];
+              const bool in = kx + row < p.kc;
+              const uint16_t *src = p.R + (static_cast<int64_t>(unit.x) * p.kc + (in ? kx + row : 0)) * p.r + unit.y + c * 8;
+              cp_async16(b_s + static_cast<uint32_t>(u) * unit_bytes +
+                             static_cast<uint32_t>(row * 2 * w + ((c ^ sw) << 4)),
+                         src, in ? 16u : 0u);
+            }
+            if (++ring == stages) {
+              ring = 0;
+              parity ^= 1u;
+            }
+          }
+          cp_async_commit();
+          if (j >= kAhead) {
+            cp_async_wait<kAhead>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[done_ring]);
+            if (++done_ring == stages) done_ring = 0;
+          }
+        }
+        cp_async_wait<0>();
+      }
       // ---------------------------------------------------------- epilogue
       if (ok) ok = mbar_wait_bounded(&acc_bar, acc_phase, p.err, kErrTimeoutAcc, 20000000000ull);
+      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
+        // Each row's own columns, 16 at a time, into the idle ring; a warp
+        // reads only the adapters its rows use.
         const int quad = warp & 3;
         const uint32_t row = static_cast<uint32_t>(quad * 32 + lane);
-        for (int c0 = 0; c0 < nu * w; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c0), v);
-          const uint32_t dst = base + (row * kPartLd + static_cast<uint32_t>(c0)) * 4u;
+        const int own = slot_of[row] - a0;
+        for (int i = 0; i < na; ++i) {
+          if (!__any_sync(0xffffffffu, own == i)) continue;
+          for (int c = 0; c < p.r; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(i * p.r + c), v);
+            if (own == i) {
+              const uint32_t dst = base + (row * part_ld + static_cast<uint32_t>(c)) * 4u;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t q[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
-            sts128(dst + 16u * static_cast<uint32_t>(j), q);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t q[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+                sts128(dst + 16u * static_cast<uint32_t>(j), q);
+              }
+            }
           }
         }
       }
     }
-    step += steps;
     acc_phase ^= 1u;
     tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     cluster_sync_all();
-    // This CTA's share of the tile's rows: each row's own adapter's columns of
-    // this pass, four at a time, the peers' partials added in rank order.
+    tc_fence_after();
+    // This CTA's share of the tile's rows, four columns at a time, the peers'
+    // partials added in rank order.
     {
       const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
-      const int left = p.m - m_tile * kRows;
-      const int valid = left < kRows ? left : kRows;
+      const int left = p.m - m_tile * p.tile_rows;
+      const int valid = left < p.tile_rows ? left : p.tile_rows;
       const int lo = valid * rank / size, hi = valid * (rank + 1) / size;
-      const int pieces = nu * w / 4;
+      const int pieces = p.r / 4;
       for (int i = threadIdx.x; i < (hi - lo) * pieces; i += kThreads) {
         const int row = lo + i / pieces, col = 4 * (i % pieces);
-        const int g = u0 + col / w;
         const int slot = slot_of[row];
-        if (slot < 0 || g / per_adapter != slot) continue;
-        const uint32_t off = base + (static_cast<uint32_t>(row) * kPartLd + static_cast<uint32_t>(col)) * 4u;
+        if (slot < a0 || slot >= a0 + na) continue;
+        const uint32_t off = base + (static_cast<uint32_t>(row) * part_ld + static_cast<uint32_t>(col)) * 4u;
         float4 part[8];
 #pragma unroll
         for (int pr = 0; pr < 8; ++pr)
           part[pr] = pr < size ? ld_dsmem_v4(off, static_cast<uint32_t>(pr)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc = part[0];
 #pragma unroll
-        for (int pr = 0; pr < 8; ++pr) {
+        for (int pr = 1; pr < 8; ++pr) {
           if (pr < size) {
             acc.x += part[pr].x;
             acc.y += part[pr].y;
@@ -305,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 2) multi_proj_kernel(const __grid_co
           }
         }
         const float s = __ldg(p.scale + list[slot]);
-        uint16_t *dst = p.out + (static_cast<int64_t>(m_tile) * kRows + row) * p.r + (g % per_adapter) * w + col % w;
+        uint16_t *dst = p.out + (static_cast<int64_t>(m_tile) * p.tile_rows + row) * p.r + col;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc.x * s, acc.y * s), pack_bf16x2(acc.z * s, acc.w * s));
       }
     }
@@ -314,20 +499,29 @@ __global__ void __launch_bounds__(kThreads, 2) multi_proj_kernel(const __grid_co
     cluster_sync_all();
   }
 
-  // Every issued copy has landed before the CTA may exit.
-  if (threadIdx.x == 0)
-    for (int j = issued - kStages < 0 ? 0 : issued - kStages; j < issued; ++j)
-      mbar_wait_bounded(&full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u, p.err, kErrTimeoutDrain);
+  // Every issued copy has landed before the CTA may exit: the products waited
+  // for them, unless there was none or a wait gave up.
+  if (!ok) failed = 1;
+  __syncthreads();
+  if (threadIdx.x == 0 && (failed || passes == 0))
+    for (int j = issued - stages < 0 ? 0 : issued - stages; j < issued; ++j) {
+      // Without a pass nobody announced the copies.
+      if (passes == 0) {
+        mbar_arrive_expect_tx(&full[j], static_cast<uint32_t>(p.tile_rows) * 128u);
+        for (int i = 0; loaders && i < 4; ++i) mbar_arrive(&full[j]);
+      }
+      mbar_wait_bounded(&full[j % stages], static_cast<uint32_t>(j / stages) & 1u, p.err, kErrTimeoutDrain);
+    }
 
   // Rows without an adapter.
   if (blockIdx.x == 0 && z == 0) {
-    const int left = p.m - m_tile * kRows;
-    const int valid = left < kRows ? left : kRows;
+    const int left = p.m - m_tile * p.tile_rows;
+    const int valid = left < p.tile_rows ? left : p.tile_rows;
     const int pieces = p.r / 8;
     for (int i = threadIdx.x; i < valid * pieces; i += kThreads) {
       const int row = i / pieces;
       if (slot_of[row] < 0)
-        reinterpret_cast<uint4 *>(p.out + (static_cast<int64_t>(m_tile) * kRows + row) * p.r)[i % pieces] =
+        reinterpret_cast<uint4 *>(p.out + (static_cast<int64_t>(m_tile) * p.tile_rows + row) * p.r)[i % pieces] =
             make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -335,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 2) multi_proj_kernel(const __grid_co
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(64u) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kMaxCols))
+                 : "memory");
   }
 }
 
@@ -384,7 +579,7 @@ cudaError_t launch(const ProjParams &p, int m_tiles, int split, cudaStream_t str
                                 configured);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.pass_ctas + (p.lists ? 1 : 0)), static_cast<unsigned>(m_tiles),
+  cfg.gridDim = dim3(static_cast<unsigned>(p.pass_ctas), static_cast<unsigned>(m_tiles),
                      static_cast<unsigned>(split));
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
@@ -403,14 +598,30 @@ cudaError_t launch(const ProjParams &p, int m_tiles, int split, cudaStream_t str
 
 }  // namespace
 
-int tile_list_rows(int64_t m) { return m <= 128 ? 128 : 512; }
+GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups) {
+  GroupRows g{};
+  int32_t *base = static_cast<int32_t *>(scratch);
+  g.groups = groups;
+  g.start = base;
+  g.count = base + groups;
+  g.list = base + (2 * static_cast<int64_t>(groups) + 63) / 64 * 64;
+  return g;
+}
 
-size_t tile_lists_bytes(int64_t m, int32_t count) { return static_cast<size_t>(carve_tile_lists(nullptr, m, count).bytes); }
+size_t group_rows_bytes(int64_t m, int32_t groups) {
+  const size_t head = (2 * static_cast<size_t>(groups) + 63) / 64 * 64;
+  return (head + 64 * (static_cast<size_t>(m) / 64 + static_cast<size_t>(groups))) * 4u;
+}
 
-TileLists carve_tile_lists(void *scratch, int64_t m, int32_t count) {
+size_t tile_lists_bytes(int64_t m, int32_t count) {
+  const int64_t a = carve_tile_lists(nullptr, m, count, 128).bytes, b = carve_tile_lists(nullptr, m, count, 512).bytes;
+  return static_cast<size_t>(a > b ? a : b);
+}
+
+TileLists carve_tile_lists(void *scratch, int64_t m, int32_t count, int32_t rows) {
   TileLists t{};
   t.base = static_cast<int32_t *>(scratch);
-  t.rows = tile_list_rows(m);
+  t.rows = rows;
   t.tiles = (m + t.rows - 1) / t.rows;
   int64_t slots = count < t.rows ? count : t.rows;
   if (m < slots) slots = m;
@@ -429,16 +640,27 @@ cudaError_t launch_multi_proj_small(const uint16_t *X, int64_t m, int64_t k, con
 }
 
 cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
-                              uint16_t *out, const TileLists *lists, cudaStream_t stream) {
+                              uint16_t *out, const TileLists *lists, const GroupRows *rows, cudaStream_t stream) {
   ProjParams p{};
-  p.width = unit_width(s.r);
-  if (!encode_bf16_map(&p.tmL, L, m, kc, 64, 128)) return cudaErrorInvalidValue;
-  if (through_b) {
-    if (!encode_bf16_stack_map(&p.tmR, s.B, s.count, kc, s.r, static_cast<uint32_t>(p.width), 64))
-      return cudaErrorInvalidValue;
-  } else if (!encode_bf16_stack_map(&p.tmR, s.A, s.count, s.r, kc, 64, static_cast<uint32_t>(p.width))) {
-    return cudaErrorInvalidValue;
+  if (rows) {
+    // Two warps beside a projection of m rows have the time for about one
+    // pass over the ids per adapter of theirs; a long batch's lists are made
+    // by more threads first.
+    if (m <= kRowsInside) {
+      p.rows = *rows;
+    } else {
+      group_rows_kernel<<<static_cast<unsigned>(s.count), kRowsThreads, 0, stream>>>(s.ids, static_cast<int>(m), *rows);
+      count_launches(1);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
   }
+  p.width = unit_width(s.r);
+  if (through_b ? p.width == 64 && !encode_bf16_stack_map(&p.tmR, s.B, s.count, kc, s.r, 64, 64)
+                : !encode_bf16_stack_map(&p.tmR, s.A, s.count, s.r, kc, 64, static_cast<uint32_t>(p.width)))
+    return cudaErrorInvalidValue;
+  p.R = s.B;
+  p.kc = kc;
   p.ids = s.ids;
   p.scale = s.scale;
   p.out = out;
@@ -452,19 +674,32 @@ cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const Ad
     p.list_stride = lists->stride;
     p.list_slots = lists->slots;
     p.list_rows = lists->rows;
-    p.list_tiles = static_cast<int>(lists->tiles);
   }
-  // Passes a tile can need at most (every row or every adapter its own), and
-  // the K split that fills about two CTAs per SM with one pass per tile; CTAs
-  // for further passes only while that leaves SMs idle.
-  const int64_t m_tiles = (m + kRows - 1) / kRows;
-  int64_t most = s.count < kRows ? s.count : kRows;
+  // One CTA per SM.  64-row tiles where 128-row ones cannot fill the SMs with
+  // clusters of 8; K is split over the largest clusters that all fit at once
+  // (a second wave would double the time).  While that leaves SMs idle and a
+  // tile may hold more adapters than one pass of 64 columns, passes stay that
+  // narrow and go to CTAs of their own; otherwise they take all the columns
+  // they can, so that X is read as few times as possible.
+  static ClusterFit fit[2];
+  const void *kernel = through_b ? reinterpret_cast<const void *>(multi_proj_kernel<true>)
+                                 : reinterpret_cast<const void *>(multi_proj_kernel<false>);
+  const auto tiles_of = [&](int64_t rows) { return (m + rows - 1) / rows; };
+  p.tile_rows = tiles_of(kRows) * 16 <= 148 ? 64 : kRows;
+  const int64_t m_tiles = tiles_of(p.tile_rows);
+  int64_t most = s.count < p.tile_rows ? s.count : p.tile_rows;      // adapters of a tile
   if (m < most) most = m;
-  const int64_t max_passes = (most * s.r + 63) / 64;
-  const int split = choose_split(m_tiles, p.nk);
-  int64_t ctas = 2 * 148 / (m_tiles * split);
-  if (ctas > max_passes) ctas = max_passes;
-  p.pass_ctas = static_cast<int>(ctas < 1 ? 1 : ctas);
+  const int most_split = p.nk / 2 < 1 ? 1 : p.nk / 2 < 8 ? p.nk / 2 : 8;
+  int clusters = 1;
+  const int split = fit[through_b].split(kernel, kThreads, kSmemBytes, m_tiles, 1, most_split, &clusters);
+  const int64_t spare = clusters / m_tiles;              // clusters per tile
+  const int narrow = s.r < 64 ? 64 / s.r : 1, wide = kMaxCols / s.r;
+  p.per_pass = spare > 1 ? narrow : wide;
+  while (p.per_pass < wide && (most + p.per_pass - 1) / p.per_pass > spare) ++p.per_pass;
+  if (p.per_pass > most) p.per_pass = static_cast<int>(most);
+  const int64_t max_passes = (most + p.per_pass - 1) / p.per_pass;
+  p.pass_ctas = static_cast<int>(spare < 1 ? 1 : spare < max_passes ? spare : max_passes);
+  if (!encode_bf16_map(&p.tmL, L, m, kc, 64, static_cast<uint32_t>(p.tile_rows))) return cudaErrorInvalidValue;
   return through_b ? launch<true>(p, static_cast<int>(m_tiles), split, stream)
                    : launch<false>(p, static_cast<int>(m_tiles), split, stream);
 }

@@ -238,41 +238,46 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       }
     }
     if constexpr (C::MULTI) {
-      // Adapter k-steps: this CTA's share of the tile's units, 64 rank columns
-      // a step; their operands come from the preceding projection.  The whole
-      // warp walks the list, lane 0 issues.
-      griddep_wait();
-      const MultiTile t = multi_tile(p.multi, 0);
-      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
-      const uint32_t w = static_cast<uint32_t>(p.multi.width);
-      const int units = t.adapters * per_adapter;
-      int lo, hi;
-      multi_share(units, per_step, &lo, &hi);
+      // Adapter k-steps: this CTA's share of the tile's.  The rank block of T
+      // or U (from the preceding projection) goes into each stage once; the
+      // input gradient's adapter rows come by TMA, the forward's from the
+      // dequant warps.
+      // The whole warp walks the list, lane 0 issues.  While
+      // lane 0 is in the main loop the others bring the adapters' rows to L2.
       AdapterWindow win;
+      const MultiTile t = multi_open(p.multi, m_tile, win, [&](int a) {
+        prefetch_adapter(p.multi, C::B_MN, a, static_cast<int64_t>(n_tile) * C::BN, C::BN, p.out_cols);
+      });
+      const MultiSteps steps(p.multi, t);
+      int lo, hi;
+      steps.share(&lo, &hi);
       int ok = __shfl_sync(0xffffffffu, issued, 0) == n_iters;
-      for (int st = lo; st < hi && ok; ++st) {
+      MultiStep at(steps, lo);
+      for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
         const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
-        const int u0 = st * per_step, nu = units - u0 < per_step ? units - u0 : per_step;
+        MultiStep step = at;
+        const bool fresh = step.since < C::STAGES;
         if (lane == 0) {
           ok = mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u, p.err,
                                  kErrTimeoutEmpty);
           if (ok) {
-            mbar_arrive_expect_tx(&full_a[s], static_cast<uint32_t>(nu) * w * (256u + 2u * C::BN));
+            mbar_arrive_expect_tx(&full_a[s],
+                                  (fresh ? C::A_BYTES : 0u) +
+                                      (C::B_MN ? (static_cast<uint32_t>(step.units) << steps.lw) * 2u * C::BN : 0u));
+            if (fresh) tma_load_2d(a_s, &p.tmA2, &full_a[s], step.block * kBK, m_tile * C::BM);
             ++issued;
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        for (int u = 0; u < nu; ++u) {
-          const int a = win.at(t, (u0 + u) / per_adapter), c = ((u0 + u) % per_adapter) * p.multi.width;
-          if (lane == 0 && ok) {
-            tma_load_2d(a_s + u * 256u * w, &p.tmA2, &full_a[s], c, m_tile * C::BM);
-            if (!C::B_MN) {
-              tma_load_3d(b_s + u * 2u * C::BN * w, &p.tmB2, &full_a[s], c, n_tile * C::BN, a);
-            } else {
+        if (C::B_MN) {
+          for (int u = 0; u < step.units; ++u, step.advance()) {
+            const int a = win.at(t, step.slot), c = step.block * 64 + (step.sub << steps.lw);
+            if (lane == 0 && ok) {
 #pragma unroll
               for (int j = 0; j < C::BN / 64; ++j)
-                tma_load_3d(b_s + j * 8192u + u * 128u * w, &p.tmB2, &full_a[s], n_tile * C::BN + 64 * j, c, a);
+                tma_load_3d(b_s + j * 8192u + (static_cast<uint32_t>(u) << steps.lw) * 128u, &p.tmB2, &full_a[s],
+                            n_tile * C::BN + 64 * j, c, a);
             }
           }
         }
@@ -313,34 +318,36 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       }
     }
     if constexpr (C::MULTI) {
-      griddep_wait();
-      const MultiTile t = multi_tile(p.multi, 0);
-      const int per_adapter = p.multi.r / p.multi.width, per_step = kBK / p.multi.width;
-      const uint32_t w = static_cast<uint32_t>(p.multi.width);
-      const int units = t.adapters * per_adapter;
-      int lo, hi;
-      multi_share(units, per_step, &lo, &hi);
       MaskWindow<1> win;
+      const MultiTile t = multi_open(p.multi, m_tile, win, [](int) {});
+      const MultiSteps steps(p.multi, t);
+      const uint32_t w = 1u << steps.lw;
+      int lo, hi;
+      steps.share(&lo, &hi);
+      MultiStep at(steps, lo);
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      for (int st = lo; st < hi && ok; ++st) {
+      for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
+        const uint32_t ph = static_cast<uint32_t>(li / C::STAGES) & 1u;
         const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
-        const int u0 = st * per_step, nu = units - u0 < per_step ? units - u0 : per_step;
-        if (lane == 0)
-          ok = mbar_wait_bounded(&full_a[s], static_cast<uint32_t>(li / C::STAGES) & 1u, p.err, kErrTimeoutFullA);
+        if (lane == 0) {
+          ok = mbar_wait_bounded(&full_a[s], ph, p.err, kErrTimeoutFullA);
+          if (ok && !C::B_MN) ok = mbar_wait_bounded(&full_b[s], ph, p.err, kErrTimeoutFullB);
+        }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (lane == 0) tc_fence_after();
-        for (int u = 0; u < nu; ++u) {
-          win.load(t, (u0 + u) / per_adapter);
+        MultiStep step = at;
+        const uint64_t ad = smem_desc(a_s, 16u, 1024u);
+        const uint64_t bd = C::B_MN ? smem_desc(b_s, 8192u, 1024u) : smem_desc_unit(b_s, 16u, 16u * w, static_cast<int>(w));
+        for (int u = 0; u < step.units; ++u, step.advance()) {
+          win.load(t, step.slot);
           if (lane == 0) {
-            for (uint32_t kk = 0; kk < w / 16u; ++kk) {
-              const uint64_t ad = smem_desc_unit(a_s + u * 256u * w + kk * 32u, 16u, 16u * w, p.multi.width);
-              const uint64_t bd = C::B_MN
-                                      ? smem_desc(b_s + u * 128u * w + kk * 2048u, 8192u, 1024u)
-                                      : smem_desc_unit(b_s + u * 2u * C::BN * w + kk * 32u, 16u, 16u * w, p.multi.width);
-              umma_f16_masked(tmem, ad, bd, C::IDESC, win.off[0]);
-            }
+            // Offsets in the descriptors' 16-byte units.
+            const uint64_t ua = ad + ((static_cast<uint32_t>(step.sub) << steps.lw) >> 3);
+            const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (C::B_MN ? 8u : 2u * C::BN / 16u);
+            for (uint32_t kk = 0; kk < w / 16u; ++kk)
+              umma_f16_masked(tmem, ua + kk * 2u, ub + kk * (C::B_MN ? 128u : 2u), C::IDESC, win.off[0]);
           }
         }
         if (lane == 0) umma_commit(&empty_bar[s]);
@@ -395,10 +402,23 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       // group count), so that a group waits on every phase of its stages'
       // barriers and a parity wait cannot be satisfied by an older phase.
       static_assert(C::DQ_GROUPS <= 1 || C::STAGES % C::DQ_GROUPS == 0, "stages per dequant group");
+      // Many adapters: the tile's list is requested two of the group's steps
+      // before the main loop ends.
+      AdapterWindow win;
+      int adapters = -1;
+      const auto open_list = [&]() {
+        if (adapters >= 0) return;
+        griddep_wait();
+        adapters = __ldcg(multi_tile_at(p.multi, m_tile));
+        win.prime(p.multi, multi_tile_at(p.multi, m_tile));
+      };
       for (int li = grp; li < n_iters; li += kStride) {
         const int it = it_begin + li;
         const int s = li % C::STAGES;
         const uint32_t ph = static_cast<uint32_t>(li / C::STAGES) & 1u;
+        if constexpr (C::MULTI && !C::B_MN) {
+          if (li + 2 * kStride >= n_iters) open_list();
+        }
         if (!mbar_wait_bounded(&full_a[s], ph, p.err, kErrTimeoutFullA)) { ok = false; break; }
         if (it < p.num_main) {
           const int64_t blk = blk_nx;
@@ -441,6 +461,35 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full_b[s]);
+      }
+      if constexpr (C::MULTI && !C::B_MN) {
+        // The adapter k-steps' rows of B_a, requested a step of the group
+        // ahead.
+        if (__all_sync(0xffffffffu, ok)) {
+          open_list();
+          const MultiTile t = multi_tile_of(p.multi, multi_tile_at(p.multi, m_tile), adapters);
+          const MultiSteps steps(p.multi, t);
+          int lo, hi;
+          steps.share(&lo, &hi);
+          const int64_t n0 = static_cast<int64_t>(n_tile) * C::BN;
+          int st = lo + ((grp - n_iters % kStride) + kStride) % kStride;     // the group's first
+          MultiStep at(steps, lo);
+          for (int i = lo; i < st; ++i) at.next(steps);
+          MultiRows<C::BN> rows;
+          if (st < hi) rows.load(p.multi, at, win, t, p.w_n, n0, dt);
+          for (; st < hi; st += kStride) {
+            const int li = n_iters + st - lo, s = li % C::STAGES;
+            ok = mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u, p.err,
+                                   kErrTimeoutEmpty);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            rows.store(p.multi, base + static_cast<uint32_t>(s) * C::STAGE_BYTES + C::A_BYTES, dt);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full_b[s]);
+            for (int i = 0; i < kStride; ++i) at.next(steps);
+            if (st + kStride < hi) rows.load(p.multi, at, win, t, p.w_n, n0, dt);
+          }
+        }
       }
     }
 
@@ -643,6 +692,39 @@ int choose_split(int64_t tiles, int ksteps, int per_sm) {
   return sp < 1 ? 1 : static_cast<int>(sp);
 }
 
+int ClusterFit::split(const void *kernel, int threads, int smem_bytes, int64_t tiles, int per_sm, int most_split,
+                      int *clusters) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  const bool slot = dev >= 0 && dev < kMaxDevicesPerProcess;
+  for (int s = most_split > 8 ? 8 : most_split; s >= 1; --s) {
+    int n = slot ? resident[dev][s].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(1, 1, static_cast<unsigned>(s));
+      cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+      cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = static_cast<unsigned>(s);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        n = sms / (2 * s) > 0 ? sms / (2 * s) : 1;
+      }
+      if (slot) resident[dev][s].store(n, std::memory_order_relaxed);
+    }
+    *clusters = n * per_sm;
+    if (n * per_sm >= tiles || s == 1) return s;
+  }
+  return 1;
+}
+
 cudaError_t tc_fwd(const uint16_t *X, int64_t m, const WeightView &w, const uint16_t *T, const uint16_t *B,
                    int32_t r, uint16_t *Y, cudaStream_t stream, bool pdl) {
   // Above 128 rows: the 256 x 256 kernel with separate operand rings.
@@ -715,18 +797,30 @@ cudaError_t tc_bwd_dx(const uint16_t *dY, int64_t m, const WeightView &w, const 
                 : launch<CfgBwd1>(p, gn, gm, stream, 1, p.pdl != 0);
 }
 
+// 512-row tiles on CTA pairs do a k-step in about 0.55 us, 128-row tiles in
+// about 0.85 us but split the k-steps over up to 8 CTAs: those are the faster
+// ones while the pairs cover less than half of the SMs (m = 300, 4096 x 4096,
+// input gradient: see the table of measurements at launch).
+int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps) {
+  if (m <= 128) return 128;
+  const int64_t gn = (cols + 255) / 256, gm = (m + 127) / 128;
+  const int64_t pair_ctas = 2 * gn * ((m + 511) / 512);
+  const int64_t tiles = gn * gm;
+  if (pair_ctas > 74 || tiles > 148) return 512;
+  const int sp = choose_split(tiles, static_cast<int>(ksteps), 1);
+  return 85 * (ksteps + sp - 1) / sp < 55 * ksteps ? 128 : 512;
+}
+
 cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
                      const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream) {
-  if (m > 128) return fused_multi_large(L, m, w, bwd, V, ad, lists, out, stream);
+  if (lists.rows != 128) return fused_multi_large(L, m, w, bwd, V, ad, lists, out, stream);
   TcParams p{};
   const int64_t in = bwd ? w.n : w.k, cols = bwd ? w.k : w.n;
   const uint32_t width = static_cast<uint32_t>(unit_width(ad.r));
   if (!encode_bf16_map(&p.tmA, L, m, in, 64, 128)) return cudaErrorInvalidValue;
   if (!encode_codes_map(&p.tmCodes, w.codes, w.n, w.k / 2, 32, bwd ? 64 : 256, false)) return cudaErrorInvalidValue;
-  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, width, 128)) return cudaErrorInvalidValue;
-  if (bwd ? !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)
-          : !encode_bf16_stack_map(&p.tmB2, ad.B, ad.count, w.n, ad.r, width, 256))
-    return cudaErrorInvalidValue;
+  if (!encode_bf16_map(&p.tmA2, V, m, ad.r, 64, 128)) return cudaErrorInvalidValue;
+  if (bwd && !encode_bf16_stack_map(&p.tmB2, ad.A, ad.count, ad.r, w.k, 64, width)) return cudaErrorInvalidValue;
   p.absmax_q = w.absmax_q;
   p.group_scale = w.group_scale;
   p.mu = w.mu;
@@ -742,10 +836,10 @@ cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd
   p.alpha = 1.0f;
   p.tab = *w.tab;
   p.multi = multi_params(ad, lists);
-  const int gn = cdiv(cols, 256);
-  const int sp = choose_split(gn, p.num_main, 1);
-  if (bwd) return sp > 1 ? launch<CfgBwd1SM>(p, gn, 1, stream, sp, true) : launch<CfgBwd1M>(p, gn, 1, stream, 1, true);
-  return sp > 1 ? launch<CfgFwd1SM>(p, gn, 1, stream, sp, true) : launch<CfgFwd1M>(p, gn, 1, stream, 1, true);
+  const int gn = cdiv(cols, 256), gm = cdiv(m, 128);
+  const int sp = choose_split(int64_t(gn) * gm, p.num_main, 1);
+  if (bwd) return sp > 1 ? launch<CfgBwd1SM>(p, gn, gm, stream, sp, true) : launch<CfgBwd1M>(p, gn, gm, stream, 1, true);
+  return sp > 1 ? launch<CfgFwd1SM>(p, gn, gm, stream, sp, true) : launch<CfgFwd1M>(p, gn, gm, stream, 1, true);
 }
 
 cudaError_t tc_proj_kmajor(const uint16_t *L, int64_t m, int64_t kc, const uint16_t *R, int32_t r, float scale,
