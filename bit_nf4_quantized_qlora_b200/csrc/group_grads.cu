@@ -33,8 +33,8 @@
 // small groups, by writing their results.
 //
 // Checkpoint form: L's tile arrives as 64 x 128 codes (half the bytes); the
-// four epilogue warps expand it to the bf16 tile the product reads, one block
-// of 64 elements (one scale) per thread: two integer and half a packed
+// eight epilogue warps expand it to the bf16 tile the product reads, half a
+// block of 64 elements (one scale) per thread: two integer and half a packed
 // floating-point instruction per element.
 #include <cuda.h>
 
@@ -47,7 +47,8 @@ namespace qlora {
 namespace {
 
 constexpr int kSlot = 64;                 // rows of a step
-constexpr int kThreads = 192;             // TMA warp, MMA warp, four expand / epilogue warps
+constexpr int kEpiWarps = 8;              // expand / result warps: four lane quadrants x two column halves
+constexpr int kThreads = 64 + 32 * kEpiWarps;     // and a TMA warp and an MMA warp
 constexpr uint32_t kLBytes = 128u * kSlot * 2u;   // bf16 tile: two 64-column slabs
 constexpr uint32_t kRBytes = 64u * kSlot * 2u;
 constexpr uint32_t kCBytes = 128u * kSlot;        // code tile
@@ -145,26 +146,21 @@ struct SlotWalk {
   }
 };
 
-// 64 accumulator columns of this thread's row.
-__device__ __forceinline__ void read_acc(uint32_t tmem, uint32_t acc, int quad, uint32_t (&v)[64]) {
-  uint32_t h[32];
-  tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64u, h);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = h[j];
-  tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64u + 32u, h);
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[32 + j] = h[j];
+// The warp's 32 accumulator columns of this thread's row.
+__device__ __forceinline__ void read_acc(uint32_t tmem, uint32_t acc, int quad, int half, uint32_t (&v)[32]) {
+  tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + acc * 64u + static_cast<uint32_t>(half * 32), v);
 }
 
-// Writes the thread's row (column p of L) of a group's [128 x 64] result.
+// Writes 32 ranks from r0 on of the thread's row (column p of L) of a group's
+// result.
 template <bool OUT_T>
 __device__ __forceinline__ void write_result(uint16_t *out, int64_t P, int r, int64_t row, int r0,
-                                             const uint32_t (&v)[64]) {
+                                             const uint32_t (&v)[32]) {
   if (!OUT_T) {
     if (row < P) {
       uint4 *dst = reinterpret_cast<uint4 *>(out + row * r + r0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4; ++j)
         if (r0 + 8 * j < r)
           dst[j] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1])),
                               pack_bf16x2(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3])),
@@ -176,7 +172,7 @@ __device__ __forceinline__ void write_result(uint16_t *out, int64_t P, int r, in
     // exchange one of two rows, so each stores a pair of columns (P is even).
     const bool odd = lane_id() & 1u;
 #pragma unroll
-    for (int j = 0; j < 64; j += 2) {
+    for (int j = 0; j < 32; j += 2) {
       const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
       const uint32_t w = odd ? pack_bf16x2(__uint_as_float(got), __uint_as_float(v[j + 1]))
                              : pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(got));
@@ -186,20 +182,20 @@ __device__ __forceinline__ void write_result(uint16_t *out, int64_t P, int r, in
   }
 }
 
-// Puts the thread's row of a partial into shared memory, along the output's
-// contiguous dimension.
+// Puts the thread's 32 columns (from col0 on) of a partial into shared memory,
+// along the output's contiguous dimension.
 template <bool OUT_T>
-__device__ __forceinline__ void store_partial(uint32_t dst, uint32_t row, const uint32_t (&v)[64]) {
+__device__ __forceinline__ void store_partial(uint32_t dst, uint32_t row, uint32_t col0, const uint32_t (&v)[32]) {
   if (!OUT_T) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const uint32_t w[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
-      sts128(dst + (row * kPartLd + 4u * static_cast<uint32_t>(j)) * 4u, w);
+      sts128(dst + (row * kPartLd + col0 + 4u * static_cast<uint32_t>(j)) * 4u, w);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (static_cast<uint32_t>(j) * 128u + row) * 4u), "r"(v[j])
+    for (int j = 0; j < 32; ++j)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + ((col0 + static_cast<uint32_t>(j)) * 128u + row) * 4u), "r"(v[j])
                    : "memory");
   }
 }
@@ -233,11 +229,11 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&expanded[s], 4);
+      mbar_init(&expanded[s], kEpiWarps);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 3; ++i) mbar_init(&acc_full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], kEpiWarps);
     fence_mbar_init();
     left_s = right_s = Part{0, 0, 0, 0, 0};
   }
@@ -311,52 +307,74 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
         mbar_wait_bounded(&full[li % kStages], static_cast<uint32_t>(li / kStages) & 1u, p.err, kErrTimeoutDrain);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // Lane 0 issues; the warp meets only where a group ends (the walk, the
+    // zeroing of its last slot's pad rows).
     GroupWalk walk(p, lo, hi);
     Part part;
-    int ok = 1, li = 0, turn = 0;
+    int ok = 1, turn = 0, s = 0;
+    uint32_t parity = 0u;
+    const uint64_t ld0 = smem_desc(base, 8192u, 1024u), rd0 = smem_desc(base + kLBytes, 8192u, 1024u);
+    const auto ready = [&]() {
+      return mbar_wait_bounded(&full[s], parity, p.err, kErrTimeoutFullA) &&
+             (!ACT8 || mbar_wait_bounded(&expanded[s], parity, p.err, kErrTimeoutFullB));
+    };
+    // The products of 16 `chunks` rows of slot s.
+    const auto multiply = [&](uint32_t acc, bool first, int chunks) {
+      tc_fence_after();
+      uint64_t ld = ld0 + static_cast<uint32_t>(s) * (kStageBytes >> 4), rd = rd0 + static_cast<uint32_t>(s) * (kStageBytes >> 4);
+      umma_f16(acc, ld, rd, kIdesc, first ? 0u : 1u);
+      for (int kk = 1; kk < chunks; ++kk) {
+        ld += 2048u / 16u;
+        rd += 2048u / 16u;
+        umma_f16(acc, ld, rd, kIdesc, 1u);
+      }
+      umma_commit(&empty[s]);
+    };
+    const auto advance = [&]() {
+      if (++s == kStages) {
+        s = 0;
+        parity ^= 1u;
+      }
+    };
     while (ok && walk.next(&part)) {
       const bool left = part.from_left();
-      const uint32_t acc = left ? kLeftAcc : static_cast<uint32_t>(turn & 1);
-      if (lane == 0 && !left)
-        ok = mbar_wait_bounded(&acc_empty[acc], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err, kErrTimeoutAcc);
-      if (!left) ++turn;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      for (int slot = part.b; slot < part.e && ok; ++slot, ++li) {
-        const int s = li % kStages;
-        const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
-        const int valid = part.rows - (slot - part.s) * kSlot;
-        const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
-        const uint32_t r_s = l_s + kLBytes;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA);
-          if (ok && ACT8) ok = mbar_wait_bounded(&expanded[s], ph, p.err, kErrTimeoutFullB);
+      const uint32_t buf = left ? kLeftAcc : static_cast<uint32_t>(turn & 1);
+      const uint32_t acc = tmem + buf * 64u;
+      // Whole slots, then (if it is in this share) a last one with pad rows.
+      const int whole = p.list ? part.s + part.rows / kSlot : part.e;
+      const int stop = whole < part.e ? whole : part.e;
+      if (lane == 0) {
+        if (!left)
+          ok = mbar_wait_bounded(&acc_empty[buf], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err, kErrTimeoutAcc);
+        for (int slot = part.b; slot < stop && ok; ++slot) {
+          ok = ready();
+          if (!ok) break;
+          multiply(acc, slot == part.b, kSlot / 16);
+          advance();
         }
+      }
+      if (!left) ++turn;
+      if (stop < part.e) {
+        if (lane == 0) ok = ok && ready();
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (p.list && valid < kSlot) {
-          // Pad rows of the group's last slot: zero rows of R (whole 128-byte
-          // rows, so the swizzle inside them does not matter).
+        if (ok) {
+          // Zero rows of R: whole 128-byte rows, so the swizzle inside them
+          // does not matter.
+          const int at = __shfl_sync(0xffffffffu, s, 0);
+          const int valid = part.rows % kSlot;
+          const uint32_t r_s = base + static_cast<uint32_t>(at) * kStageBytes + kLBytes;
           const uint32_t zero[4] = {0u, 0u, 0u, 0u};
           for (int c = valid * 8 + lane; c < kSlot * 8; c += 32) sts128(r_s + static_cast<uint32_t>(c) * 16u, zero);
           fence_proxy_async_smem();
           __syncwarp();
-        }
-        if (lane == 0) {
-          tc_fence_after();
-          const int chunks = valid >= kSlot ? kSlot / 16 : (valid + 15) / 16;
-          uint64_t ld = smem_desc(l_s, 8192u, 1024u), rd = smem_desc(r_s, 8192u, 1024u);
-          umma_f16(tmem + acc * 64u, ld, rd, kIdesc, slot > part.b ? 1u : 0u);
-#pragma unroll
-          for (int kk = 1; kk < kSlot / 16; ++kk) {
-            ld += 2048u / 16u;
-            rd += 2048u / 16u;
-            if (kk < chunks) umma_f16(tmem + acc * 64u, ld, rd, kIdesc, 1u);
+          if (lane == 0) {
+            multiply(acc, stop == part.b, (valid + 15) / 16);
+            advance();
           }
-          umma_commit(&empty[s]);
-          if (slot + 1 == part.e) umma_commit(&acc_full[acc]);
         }
-        __syncwarp();
       }
+      if (lane == 0 && ok) umma_commit(&acc_full[buf]);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else {
     const int t = static_cast<int>(threadIdx.x) - 64;
@@ -364,8 +382,9 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     // The expansion and the results share these warps: after a group's last
     // slot is expanded its result is not waited for until the next group's
     // slots that fit the ring are expanded too.
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - 2) >> 2;      // TMEM lanes, 32 of the 64 columns
     const uint32_t row = static_cast<uint32_t>(quad * 32 + lane);
+    const int rc = r0 + 32 * half;
     GroupWalk results(p, lo, z + 1 == nz ? 0x7FFFFFFF : hi);
     int turn = 0;
     Part part;
@@ -377,10 +396,10 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       while (ok && more && done + (part.live() ? part.e - part.b : 0) <= expanded_slots) {
         uint16_t *out = p.out + static_cast<int64_t>(part.group) * p.P * p.r;
         if (!part.live()) {
-          uint32_t v[64];
+          uint32_t v[32];
 #pragma unroll
-          for (int j = 0; j < 64; ++j) v[j] = 0u;
-          write_result<OUT_T>(out, p.P, p.r, p0 + row, r0, v);
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+          write_result<OUT_T>(out, p.P, p.r, p0 + row, rc, v);
         } else if (part.from_left()) {
           if (t == 0) left_s = part;
         } else {
@@ -392,12 +411,12 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             tc_fence_after();
-            uint32_t v[64];
-            read_acc(tmem, static_cast<uint32_t>(turn & 1), quad, v);
+            uint32_t v[32];
+            read_acc(tmem, static_cast<uint32_t>(turn & 1), quad, half, v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[turn & 1]);
-            write_result<OUT_T>(out, p.P, p.r, p0 + row, r0, v);
+            write_result<OUT_T>(out, p.P, p.r, p0 + row, rc, v);
           }
           ++turn;
         }
@@ -407,9 +426,9 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     };
     if (ACT8) {
       // ---------------------------------------------------------- expand
-      // Thread t: row t / 2 of the slot, 64-column half t % 2.
-      const int erow = t >> 1, half = t & 1;
-      const int64_t kb = p.P / 64, cb = static_cast<int64_t>(p_tile) * 2 + half;
+      // Thread t: row t / 4 of the slot, 32-column quarter t % 4.
+      const int erow = t >> 2, quarter = t & 3, slab = quarter >> 1;
+      const int64_t kb = p.P / 64, cb = static_cast<int64_t>(p_tile) * 2 + slab;
       const uint32_t sw = static_cast<uint32_t>(erow & 7);
       const auto row_of = [&](int slot) -> int64_t {
         if (slot < 0) return -1;
@@ -417,43 +436,46 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
         return p.list ? __ldg(p.list + i) : (i < p.m ? i : -1);
       };
       const auto scale_of = [&](int64_t gr) -> uint32_t {
-        return (gr >= 0 && cb < kb) ? static_cast<uint32_t>(__ldg(p.scale + gr * kb + cb)) * 0x10001u : 0u;
+        return (gr >= 0 && cb < kb) ? static_cast<uint32_t>(__ldg(p.scale + gr * kb + cb)) : 0u;
       };
-      // Row numbers two slots ahead, scales one slot ahead.
+      // Scales two slots ahead, row numbers three: requested after a slot's
+      // proxy fence, which would wait for them.
       SlotWalk walk(p, lo, hi);
-      int slot = walk.next(), slot_nx = slot < 0 ? -1 : walk.next();
-      uint32_t s_nx = scale_of(row_of(slot));
-      int64_t row_nx = row_of(slot_nx);
+      int slot = walk.next(), slot1 = slot < 0 ? -1 : walk.next(), slot2 = slot1 < 0 ? -1 : walk.next();
+      uint32_t s0 = scale_of(row_of(slot)), s1 = scale_of(row_of(slot1));
+      int64_t row2 = row_of(slot2);
       for (int li = 0; slot >= 0; ++li) {
         const int s = li % kStages;
         const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
-        const uint32_t s2 = s_nx;
-        s_nx = scale_of(row_nx);
-        slot = slot_nx;
-        slot_nx = slot < 0 ? -1 : walk.next();
-        row_nx = row_of(slot_nx);
+        const uint32_t s2 = s0 * 0x10001u;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA));
         if (!ok) break;
         const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
         const uint32_t code_row = l_s + kLBytes + kRBytes + static_cast<uint32_t>(erow) * 128u;
-        const uint32_t out_row = l_s + static_cast<uint32_t>(half) * 8192u + static_cast<uint32_t>(erow) * 128u;
+        const uint32_t out_row = l_s + static_cast<uint32_t>(slab) * 8192u + static_cast<uint32_t>(erow) * 128u;
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          // 16 codes -> two 16-byte chunks; the halves walk them in an order
+        for (int jj = 0; jj < 2; ++jj) {
+          // 16 codes -> two 16-byte chunks; the slabs walk them in an order
           // that keeps a quarter-warp's stores in distinct bank groups.
-          const uint32_t j = static_cast<uint32_t>(jj ^ (2 * half));
-          const uint4 c = lds128(code_row + (((4u * half + j) ^ sw) << 4));
+          const uint32_t j = static_cast<uint32_t>(jj ^ slab), at = 4u * (quarter & 1) + 2u * j;
+          const uint4 c = lds128(code_row + (((2u * quarter + j) ^ sw) << 4));
           uint32_t o[4];
           act8_decode4(c.x, s2, o[0], o[1]);
           act8_decode4(c.y, s2, o[2], o[3]);
-          sts128(out_row + (((2u * j) ^ sw) << 4), o);
+          sts128(out_row + ((at ^ sw) << 4), o);
           act8_decode4(c.z, s2, o[0], o[1]);
           act8_decode4(c.w, s2, o[2], o[3]);
-          sts128(out_row + (((2u * j + 1u) ^ sw) << 4), o);
+          sts128(out_row + (((at + 1u) ^ sw) << 4), o);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&expanded[s]);
+        s0 = s1;
+        s1 = scale_of(row2);
+        slot = slot1;
+        slot1 = slot2;
+        slot2 = slot2 < 0 ? -1 : walk.next();
+        row2 = row_of(slot2);
         // Results two slots late: their products have had time to finish.
         flush(li - 1);
         if (!ok) break;
@@ -463,7 +485,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     if (ok) flush(0x7FFFFFFF);
     // Partials of the groups that cross the share's borders, into the idle
     // ring: every product of the share is done once the last accumulator is.
-    named_barrier_sync(1, 128);
+    named_barrier_sync(1, 32 * kEpiWarps);
     const bool left = left_s.live(), right = right_s.live();
     if (ok && right)
       ok = mbar_wait_bounded(&acc_full[(turn - 1) & 1], static_cast<uint32_t>((turn - 1) >> 1) & 1u, p.err,
@@ -472,14 +494,14 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     ok = __all_sync(0xffffffffu, ok);
     if (ok && (left || right)) {
       tc_fence_after();
-      uint32_t v[64];
+      uint32_t v[32];
       if (left) {
-        read_acc(tmem, kLeftAcc, quad, v);
-        store_partial<OUT_T>(base, row, v);
+        read_acc(tmem, kLeftAcc, quad, half, v);
+        store_partial<OUT_T>(base, row, 32u * half, v);
       }
       if (right) {
-        read_acc(tmem, static_cast<uint32_t>((turn - 1) & 1), quad, v);
-        store_partial<OUT_T>(base + kPartBytes, row, v);
+        read_acc(tmem, static_cast<uint32_t>((turn - 1) & 1), quad, half, v);
+        store_partial<OUT_T>(base + kPartBytes, row, 32u * half, v);
       }
     }
   }
