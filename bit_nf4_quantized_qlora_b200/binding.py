@@ -494,9 +494,9 @@ class Act8:
 
 
 def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device: torch.device) -> None:
-    """The tensor is a contiguous tensor of this type and shape on this CUDA
-    device."""
-    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device and t.is_cuda):
+    """The tensor is a contiguous tensor of this type and shape on this device
+    (which _stream_on then finds to be the current CUDA device)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors must be contiguous CUDA tensors")
@@ -517,6 +517,10 @@ def _need_weight(w: NF4Weight, device) -> None:
         raise ValueError(f"the weight is on {w.codes.device}, not on {device}")
 
 
+def _out(t: Optional[torch.Tensor], shape, device) -> torch.Tensor:
+    return torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t
+
+
 def _need_ws(ws: Optional[torch.Tensor], device) -> None:
     if ws is not None and (ws.device != device or not ws.is_contiguous()):
         _need_cuda(ws)
@@ -526,6 +530,8 @@ def _need_ws(ws: Optional[torch.Tensor], device) -> None:
 def _stream_on(device: torch.device, stream) -> Optional[int]:
     """The stream's handle; the default is the current stream of the tensors'
     device, which must be the current device (the library launches there)."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be contiguous CUDA tensors")
     if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
@@ -550,8 +556,7 @@ def qlora_act_dequant(act: Act8, out: Optional[torch.Tensor] = None, stream=None
     """The checkpoint's X^ = bf16(codes . scale) [m x k]."""
     dev = act.codes.device
     _need_act8(act, act.m, act.k, dev)
-    if out is None:
-        out = torch.empty(act.m, act.k, dtype=torch.bfloat16, device=dev)
+    out = _out(out, (act.m, act.k), dev)
     _need(out, "out", torch.bfloat16, (act.m, act.k), dev)
     a = act.c_struct()
     _check("qlora_act_dequant", lib().qlora_act_dequant(ctypes.byref(a), out.data_ptr(), _stream_on(dev, stream)))
@@ -565,12 +570,9 @@ def qlora_linear_bwd_act8(dY: torch.Tensor, act: Act8, w: NF4Weight, A: torch.Te
     """(dX or None, dA, dB) as qlora_linear_bwd with X read from its 8-bit
     checkpoint; T = the forward's bf16(s X A^T) [m x r]."""
     m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
-    if dX is None and want_dx:
-        dX = torch.empty(m, k, dtype=bf, device=dev)
-    if dA is None:
-        dA = torch.empty(r, k, dtype=bf, device=dev)
-    if dB is None:
-        dB = torch.empty(n, r, dtype=bf, device=dev)
+    if dX is not None or want_dx:
+        dX = _out(dX, (m, k), dev)
+    dA, dB = _out(dA, (r, k), dev), _out(dB, (n, r), dev)
     for t, name, shape in ((dY, "dY", (m, n)), (A, "A", (r, k)), (B, "B", (n, r)), (T, "T", (m, r)),
                            (dX, "dX", (m, k)), (dA, "dA", (r, k)), (dB, "dB", (n, r))):
         _need(t, name, bf, shape, dev)
@@ -619,8 +621,7 @@ def qlora_linear_fwd_multi(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: to
     B [count x n x r], scale fp32 [count], ids int32 [m].  The first m*r*2
     bytes of `ws` hold T afterwards."""
     m, dev = X.shape[0], X.device
-    if out is None:
-        out = torch.empty(m, w.n, dtype=torch.bfloat16, device=dev)
+    out = _out(out, (m, w.n), dev)
     _need(X, "X", torch.bfloat16, (m, w.k), dev)
     _need(out, "out", torch.bfloat16, (m, w.n), dev)
     set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
@@ -641,12 +642,9 @@ def qlora_linear_bwd_multi(dY: torch.Tensor, X, w: NF4Weight, A: torch.Tensor, B
     input or its Act8 checkpoint; T the forward's, required with a checkpoint."""
     m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
     set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
-    if dX is None and want_dx:
-        dX = torch.empty(m, k, dtype=bf, device=dev)
-    if dA is None:
-        dA = torch.empty(count, r, k, dtype=bf, device=dev)
-    if dB is None:
-        dB = torch.empty(count, n, r, dtype=bf, device=dev)
+    if dX is not None or want_dx:
+        dX = _out(dX, (m, k), dev)
+    dA, dB = _out(dA, (count, r, k), dev), _out(dB, (count, n, r), dev)
     act = X if isinstance(X, Act8) else None
     if act is not None:
         _need_act8(act, m, k, dev)
