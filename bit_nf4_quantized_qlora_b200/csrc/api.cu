@@ -617,9 +617,10 @@ int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight 
     if (e == cudaSuccess) e = launch_small_m(X, m, w, T, a->B, a->r, Y, s, true, ids, a->count);
   } else {
     const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
+    const int64_t steps = w->k / 64;
     const TileLists lists =
-        carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count, multi_tile_rows(m, w->n, w->k / 64));
-    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, nullptr, s);
+        carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count, multi_tile_rows(m, w->n, steps));
+    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, nullptr, multi_grid(m, w->n, steps, lists.rows), s);
     if (e == cudaSuccess) e = tc_multi(X, m, view(w), false, T, ad, lists, Y, s);
   }
   return cuda_status(e);
@@ -660,12 +661,15 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
   uint8_t *p = static_cast<uint8_t *>(ws);
   uint16_t *U = reinterpret_cast<uint16_t *>(p), *Tw = reinterpret_cast<uint16_t *>(p + mr);
-  const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, (n + 63) / 64));
+  const int64_t steps = (n + 63) / 64;
+  const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, steps));
   const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), m, a->count);
   cudaError_t e = cudaSuccess;
-  if (!T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, nullptr, s);                          // T = s_a X A_a^T
-  if (e == cudaSuccess) e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, &rows, s);  // U = s_a dY B_a
-  if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);                 // dX = dY W^ + U A_a
+  if (!T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, nullptr, MultiGrid{}, s);    // T = s_a X A_a^T
+  if (e == cudaSuccess)                                                                       // U = s_a dY B_a
+    e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, &rows,
+                          dX ? multi_grid(m, k, steps, lists.rows) : MultiGrid{}, s);
+  if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);        // dX = dY W^ + U A_a
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
   if (e == cudaSuccess)
     e = launch_group_grads(X, X8 ? &x8 : nullptr, U, k, dA, dY, T ? T : Tw, n, dB, m, a->r, &rows, s);

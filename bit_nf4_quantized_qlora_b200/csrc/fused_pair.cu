@@ -79,6 +79,7 @@ constexpr uint32_t kBRing = kStages * kABytes;                            // 128
 constexpr uint32_t kCRing = kBRing + kStages * kBBytes;                   // 192 KB
 constexpr uint32_t kSmemBytes = kCRing + kCodeSlots * kCBytes + 1024u;
 constexpr int kThreads = 32 * (kFirstDqWarp + kGroups * kGroupWarps);
+constexpr int kScoutWarp = kThreads / 32;       // many adapters: one more warp reads the tile's list
 constexpr uint32_t kTmemCols = 512;             // two 128 x 256 fp32 accumulators per CTA
 static_assert(kStages == kGroups && kCodeSlots % kGroups == 0, "each dequant group owns its slots");
 static_assert(kSmemBytes <= 227u * 1024u, "shared memory");
@@ -106,12 +107,14 @@ struct __align__(64) PairParams {
 // MULTI: the rows' adapters differ; the adapter k-steps follow the list of
 // the pair's 512-row tile, each unit's product masked to its adapter's rows.
 template <bool BWD, bool MULTI>
-__global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_constant__ PairParams p) {
+__global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_kernel(const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t xfull[kStages], wfull[kStages], empty[kStages];
   __shared__ __align__(8) uint64_t cfull[kCodeSlots], cempty[kCodeSlots];
   __shared__ __align__(8) uint64_t acc_full;
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) uint8_t list_smem[MULTI ? sizeof(MultiListSmem<4>) : 16];
+  MultiListSmem<4> &list = *reinterpret_cast<MultiListSmem<4> *>(list_smem);
   constexpr uint32_t kIdesc = make_idesc(kBN, false, BWD, 256);
 
   const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
@@ -137,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
       mbar_init(&cempty[c], kGroupWarps);
     }
     mbar_init(&acc_full, 1);
+    if (MULTI) mbar_init(&list.ready, 1);
     fence_mbar_init();
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmCodes);
@@ -199,15 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
       // Adapter k-steps of the tile's list.  This CTA's rows of a rank block
       // of T or U go into each activation slot once; the input gradient's
       // adapter rows come by TMA, the forward's from the dequant warps.  The
-      // whole warp walks the list, lane 0 issues.  While lane 0 is in the main
-      // loop the others bring the adapters' rows to L2.
+      // whole warp walks the list, lane 0 issues.
       AdapterWindow win;
-      const MultiTile t = multi_open(p.multi, m_pair, win, [&](int a) {
-        prefetch_adapter(p.multi, BWD, a, c0, kHalfN, p.out_cols);
-      });
+      MultiTile t{};
+      int ok = multi_open(p.multi, m_pair, list, p.err, &t) && __shfl_sync(0xffffffffu, issued, 0) == total;
       const MultiSteps steps(p.multi, t);
+      griddep_wait();      // the copies of T or U; the list is there, so the projection is done
       const int n_steps = steps.count();
-      int ok = __shfl_sync(0xffffffffu, issued, 0) == total;
       MultiStep at(steps, 0);
       for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
         const int it = total + st, s = it % kStages;
@@ -306,12 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     if constexpr (MULTI) {
       if (leader) {
         MaskWindow<4> win;
-        const MultiTile t = multi_open(p.multi, m_pair, win, [](int) {});
+        MultiTile t{};
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = multi_open(p.multi, m_pair, list, p.err, &t) && ok;
         const MultiSteps steps(p.multi, t);
         const uint32_t w = 1u << steps.lw;
         const int n_steps = steps.count();
         MultiStep at(steps, 0);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
         for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
           const int it = total + st, s = it % kStages;
           const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
@@ -349,6 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     if (leader && lane == 0) {
       if (ok) umma_commit_pair_both(&acc_full);
     }
+  } else if (MULTI && warp == kScoutWarp) {
+    if constexpr (MULTI)
+      multi_scout(p.multi, m_pair, list, [&](int a) { prefetch_adapter(p.multi, BWD, a, c0, kHalfN, p.out_cols); });
   } else {
     // ------------------------------------------------------------ dequant
     const int dq = warp - kFirstDqWarp;
@@ -387,21 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     float S_nx = blk_nx >= 0 ? __ldg(p.group_scale + (blk_nx >> 8)) : 0.f;
     int64_t g_cur = -1;
     float t_cur = 0.f;
-    // Many adapters: the tile's list is requested two of the group's steps
-    // before the main loop ends.
-    AdapterWindow win;
-    int adapters = -1;
-    const auto open_list = [&]() {
-      if (adapters >= 0) return;
-      griddep_wait();
-      adapters = __ldcg(multi_tile_at(p.multi, m_pair));
-      win.prime(p.multi, multi_tile_at(p.multi, m_pair));
-    };
     for (int it = grp; it < total; it += kGroups) {
       const uint32_t use = static_cast<uint32_t>(it / kStages);
-      if constexpr (MULTI && !BWD) {
-        if (it + 2 * kGroups >= total) open_list();
-      }
       if (it < p.num_main) {
         const int c = it % kCodeSlots;
         if (!mbar_wait_bounded(&cfull[c], static_cast<uint32_t>(it / kCodeSlots) & 1u, p.err, kErrTimeoutFullA))
@@ -461,10 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) fused_pair_kernel(const __grid_co
     if constexpr (MULTI && !BWD) {
       // The adapter k-steps' rows of B_a (this CTA's half tile), requested a
       // step of the group ahead.
-      open_list();
-      const MultiTile t = multi_tile_of(p.multi, multi_tile_at(p.multi, m_pair), adapters);
+      AdapterWindow win;
+      MultiTile t{};
+      const bool listed = multi_open(p.multi, m_pair, list, p.err, &t);
       const MultiSteps steps(p.multi, t);
-      const int n_steps = steps.count();
+      const int n_steps = listed ? steps.count() : 0;
       int st = ((grp - total % kGroups) + kGroups) % kGroups;
       MultiStep at(steps, 0);
       for (int i = 0; i < st; ++i) at.next(steps);
@@ -547,7 +541,7 @@ cudaError_t launch_pair(const PairParams &p, int64_t m, int64_t out_cols, cudaSt
   const int64_t pairs_m = (m + 2 * kRowsCta - 1) / (2 * kRowsCta);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs_m), static_cast<unsigned>((out_cols + kBN - 1) / kBN), 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads + (MULTI ? 32 : 0), 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -220,8 +220,11 @@ struct ClusterFit {
   // The largest cluster size <= most_split of which `tiles` fit at once (1 if
   // none does), with per_sm CTAs to an SM (the runtime counts one);
   // *clusters is how many of that size do.
+  // With `most_sms` below the device's, of which so many fit on that many SMs;
+  // their size is even then (or 1): the CTA pairs of another kernel find whole
+  // pairs of SMs beside them.
   int split(const void *kernel, int threads, int smem_bytes, int64_t tiles, int per_sm, int most_split,
-            int *clusters);
+            int *clusters, int most_sms = 1 << 30);
 };
 
 // Many adapters on one weight -------------------------------------------------
@@ -254,8 +257,16 @@ int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps);
 // bf16(s_a . L . B_a) (L = dY [m x n]); zeros in rows without an adapter.
 // Fills `lists` and `rows` too unless null.  m > 0.
 struct GroupRows;
+// `next` is the product launched on its heels, if any (see multi_grid).
+struct MultiGrid {
+  int64_t ctas;     // one to an SM
+  int64_t steps;    // 64-wide k-steps of each before it needs the projection
+};
 cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
-                              uint16_t *out, const TileLists *lists, const GroupRows *rows, cudaStream_t stream);
+                              uint16_t *out, const TileLists *lists, const GroupRows *rows, MultiGrid next,
+                              cudaStream_t stream);
+// tc_multi's grid on tiles of `rows` rows (multi_tile_rows).
+MultiGrid multi_grid(int64_t m, int64_t cols, int64_t ksteps, int rows);
 // The first form for m <= 16 (no lists).
 cudaError_t launch_multi_proj_small(const uint16_t *X, int64_t m, int64_t k, const AdapterView &s, uint16_t *T,
                                     cudaStream_t stream);

@@ -123,64 +123,94 @@ inline MultiParams multi_params(const AdapterView &ad, const TileLists &l) {
   return MultiParams{l.base, l.stride, l.slots, l.rows, ad.r, unit_width(ad.r), ad.A, ad.B};
 }
 
-// One tile's list.  Written by the kernel this one overlaps: read only after
-// griddep_wait, and past L1.
+// One tile's list: its first entries (adapter ids and the masks of QUADS * 128
+// rows) in shared memory, as many as the kernels have room for, the rest where
+// the projection wrote them.
+constexpr int kListEntries = 24;
+template <int QUADS>
+struct MultiListSmem {
+  uint64_t ready;
+  int adapters, pad;
+  int id[kListEntries];
+  uint4 mask[kListEntries * QUADS];
+};
 struct MultiTile {
   const int32_t *list;
   const uint4 *mask;
+  const int *id_smem;
+  const uint4 *mask_smem;
   int adapters;
 };
 __device__ __forceinline__ const int32_t *multi_tile_at(const MultiParams &p, int tile) {
   return p.lists + tile * p.stride;
 }
-__device__ __forceinline__ MultiTile multi_tile_of(const MultiParams &p, const int32_t *t, int adapters) {
-  return MultiTile{t + 4, reinterpret_cast<const uint4 *>(t + 4 + p.slots), adapters};
+
+// The warp of a kernel that overlaps the projection, for all of its others:
+// waits for the projection (which stops a whole warp, so no warp of the main
+// loop may), takes the list and passes its adapters to `prefetch`, whose rows
+// are in L2 when the main loop ends.  Reads past L1: the lists were written
+// while this kernel ran.
+template <int QUADS, class Prefetch>
+__device__ __forceinline__ void multi_scout(const MultiParams &p, int tile, MultiListSmem<QUADS> &s,
+                                            const Prefetch &prefetch) {
+  griddep_wait();
+  const int32_t *t = multi_tile_at(p, tile);
+  const uint4 *mask = reinterpret_cast<const uint4 *>(t + 4 + p.slots);
+  const int lane = static_cast<int>(lane_id()), n = __ldcg(t);
+  if (lane < p.slots && lane < kListEntries) {
+    s.id[lane] = __ldcg(t + 4 + lane);
+#pragma unroll
+    for (int q = 0; q < QUADS; ++q) s.mask[lane * QUADS + q] = __ldcg(mask + lane * QUADS + q);
+  }
+  if (lane == 0) s.adapters = n;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&s.ready);
+  for (int i = lane; i < n; i += 32) prefetch(__ldcg(t + 4 + i));
+}
+// The list in one of the other warps; false if the wait for it ran out.
+template <int QUADS>
+__device__ __forceinline__ bool multi_open(const MultiParams &p, int tile, MultiListSmem<QUADS> &s, unsigned *err,
+                                           MultiTile *out) {
+  __syncwarp();
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s.ready, 0u, err, kErrTimeoutFullA))) return false;
+  const int32_t *t = multi_tile_at(p, tile);
+  *out = MultiTile{t + 4, reinterpret_cast<const uint4 *>(t + 4 + p.slots), s.id, s.mask, s.adapters};
+  return true;
 }
 
 // A warp's window on the list, so that the latency of a list read is paid once
-// per 32 adapters: entry first + i is in lane (i + 1) % 32.  Lane 0 runs the
-// main loop in the warps that issue copies and products; entries 0 .. 30 are
-// with the lanes that have been idle since the start.  Called by whole warps.
+// per 32 adapters: entry first + i is in lane i.  Called by whole warps.
 struct AdapterWindow {
   int first = -32, id = 0;
-  __device__ __forceinline__ void prime(const MultiParams &p, const int32_t *t) {
-    first = 0;
-    const int i = (static_cast<int>(lane_id()) + 31) & 31;
-    id = i < p.slots && (i < 31 || p.slots > 31) ? __ldcg(t + 4 + i) : 0;
-  }
   __device__ __forceinline__ int at(const MultiTile &t, int slot) {
     if (slot < first || slot >= first + 32) {
-      first = slot;
-      const int i = slot + ((static_cast<int>(lane_id()) + 31) & 31);
-      id = i < t.adapters ? __ldcg(t.list + i) : 0;
+      first = slot & ~31;
+      const int i = first + static_cast<int>(lane_id());
+      id = i >= t.adapters ? 0 : i < kListEntries ? t.id_smem[i] : __ldcg(t.list + i);
     }
-    return __shfl_sync(0xffffffffu, id, (slot - first + 1) & 31);
+    return __shfl_sync(0xffffffffu, id, slot - first);
   }
 };
-// Likewise the row masks of QUADS * 128 rows; off[q] is the lane mask of rows
-// 128 q .. of the tile: set where the row is not the adapter's.
+// Likewise the row masks; off[q] is the lane mask of rows 128 q .. of the
+// tile: set where the row is not the adapter's.
 template <int QUADS>
 struct MaskWindow {
   int first = -32, current = -1;
   uint4 on[QUADS];
   uint4 off[QUADS];
-  __device__ __forceinline__ void prime(const MultiParams &p, const int32_t *t) {
-    first = 0;
-    const int i = (static_cast<int>(lane_id()) + 31) & 31;
-    const uint4 *mask = reinterpret_cast<const uint4 *>(t + 4 + p.slots);
-#pragma unroll
-    for (int q = 0; q < QUADS; ++q) on[q] = i < p.slots ? __ldcg(mask + i * QUADS + q) : make_uint4(0u, 0u, 0u, 0u);
-  }
   __device__ __forceinline__ void load(const MultiTile &t, int slot) {
     if (slot == current) return;
     current = slot;
     if (slot < first || slot >= first + 32) {
-      first = slot;
-      const int i = slot + ((static_cast<int>(lane_id()) + 31) & 31);
+      first = slot & ~31;
+      const int i = first + static_cast<int>(lane_id());
 #pragma unroll
-      for (int q = 0; q < QUADS; ++q) on[q] = i < t.adapters ? __ldcg(t.mask + i * QUADS + q) : make_uint4(0u, 0u, 0u, 0u);
+      for (int q = 0; q < QUADS; ++q)
+        on[q] = i >= t.adapters ? make_uint4(0u, 0u, 0u, 0u)
+                : i < kListEntries ? t.mask_smem[i * QUADS + q]
+                                   : __ldcg(t.mask + i * QUADS + q);
     }
-    const int l = (slot - first + 1) & 31;
+    const int l = slot - first;
 #pragma unroll
     for (int q = 0; q < QUADS; ++q)
       off[q] = make_uint4(~__shfl_sync(0xffffffffu, on[q].x, l), ~__shfl_sync(0xffffffffu, on[q].y, l),
@@ -188,20 +218,6 @@ struct MaskWindow {
   }
 };
 
-// Opens a tile in a warp whose lane 0 arrives late: the other lanes read the
-// list as soon as its kernel is done and pass its adapters to `prefetch`.
-template <class Window, class Prefetch>
-__device__ __forceinline__ MultiTile multi_open(const MultiParams &p, int tile, Window &win, const Prefetch &prefetch) {
-  griddep_wait();
-  const int32_t *t = multi_tile_at(p, tile);
-  const int lane = static_cast<int>(lane_id());
-  int n = lane != 0 ? __ldcg(t) : 0;
-  win.prime(p, t);
-  if (lane != 0)
-    for (int i = lane - 1; i < n; i += 31) prefetch(__ldcg(t + 4 + i));
-  n = __shfl_sync(0xffffffffu, n, 1);
-  return multi_tile_of(p, t, n);
-}
 // `bytes` (a multiple of 16) at `src` into L2.
 __device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");

@@ -640,7 +640,8 @@ cudaError_t launch_multi_proj_small(const uint16_t *X, int64_t m, int64_t k, con
 }
 
 cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
-                              uint16_t *out, const TileLists *lists, const GroupRows *rows, cudaStream_t stream) {
+                              uint16_t *out, const TileLists *lists, const GroupRows *rows, MultiGrid next,
+                              cudaStream_t stream) {
   ProjParams p{};
   if (rows) {
     // Two warps beside a projection of m rows have the time for about one
@@ -681,19 +682,24 @@ cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const Ad
   // tile may hold more adapters than one pass of 64 columns, passes stay that
   // narrow and go to CTAs of their own; otherwise they take all the columns
   // they can, so that X is read as few times as possible.
+  int64_t most = s.count < kRows ? s.count : kRows;                  // adapters of a tile
+  if (m < most) most = m;
+  const int narrow = s.r < 64 ? 64 / s.r : 1, wide = kMaxCols / s.r;
+  const auto tiles_of = [&](int64_t rows) { return (m + rows - 1) / rows; };
+  int sms = 148;
+  const int64_t free_sms = next.ctas > 0 ? 148 - next.ctas : 0;
+  if (free_sms >= 16 && tiles_of(kRows) * ((most + wide - 1) / wide) * p.nk <= free_sms * next.steps)
+    sms = static_cast<int>(free_sms);
   static ClusterFit fit[2];
   const void *kernel = through_b ? reinterpret_cast<const void *>(multi_proj_kernel<true>)
                                  : reinterpret_cast<const void *>(multi_proj_kernel<false>);
-  const auto tiles_of = [&](int64_t rows) { return (m + rows - 1) / rows; };
-  p.tile_rows = tiles_of(kRows) * 16 <= 148 ? 64 : kRows;
+  p.tile_rows = tiles_of(kRows) * 16 <= sms ? 64 : kRows;
+  if (most > p.tile_rows) most = p.tile_rows;
   const int64_t m_tiles = tiles_of(p.tile_rows);
-  int64_t most = s.count < p.tile_rows ? s.count : p.tile_rows;      // adapters of a tile
-  if (m < most) most = m;
   const int most_split = p.nk / 2 < 1 ? 1 : p.nk / 2 < 8 ? p.nk / 2 : 8;
   int clusters = 1;
-  const int split = fit[through_b].split(kernel, kThreads, kSmemBytes, m_tiles, 1, most_split, &clusters);
+  const int split = fit[through_b].split(kernel, kThreads, kSmemBytes, m_tiles, 1, most_split, &clusters, sms);
   const int64_t spare = clusters / m_tiles;              // clusters per tile
-  const int narrow = s.r < 64 ? 64 / s.r : 1, wide = kMaxCols / s.r;
   p.per_pass = spare > 1 ? narrow : wide;
   while (p.per_pass < wide && (most + p.per_pass - 1) / p.per_pass > spare) ++p.per_pass;
   if (p.per_pass > most) p.per_pass = static_cast<int>(most);

@@ -108,7 +108,8 @@ struct Cfg {
   // The masked-add epilogue regenerates the dropout mask (one Philox call per
   // 16 outputs): sixteen warps share that work.
   static constexpr int NUM_EPI_WARPS = B_NF4 ? 8 * DQ_GROUPS : (EPI == kEpiDropoutAdd ? 16 : 4);
-  static constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
+  // With many adapters one more warp reads the tile's list.
+  static constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS + (MULTI ? 32 : 0);
   static constexpr uint32_t TMEM_RAW = static_cast<uint32_t>(BN * MSUB);
   static constexpr uint32_t TMEM_COLS = TMEM_RAW <= 32 ? 32 : TMEM_RAW <= 64 ? 64 : TMEM_RAW <= 128 ? 128 : TMEM_RAW <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC = make_idesc(BN, A_MN, B_MN);
@@ -136,6 +137,8 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t acc_bar;
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) uint8_t list_smem[C::MULTI ? sizeof(MultiListSmem<1>) : 16];
+  MultiListSmem<1> &list = *reinterpret_cast<MultiListSmem<1> *>(list_smem);
 
   const uint32_t raw = smem_u32(dsmem);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -163,6 +166,7 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(&acc_bar, 1);
+    if (C::MULTI) mbar_init(&list.ready, 1);
     fence_mbar_init();
     tma_prefetch_desc(&p.tmA);
     if (C::B_NF4) tma_prefetch_desc(&p.tmCodes); else tma_prefetch_desc(&p.tmB);
@@ -242,16 +246,14 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       // or U (from the preceding projection) goes into each stage once; the
       // input gradient's adapter rows come by TMA, the forward's from the
       // dequant warps.
-      // The whole warp walks the list, lane 0 issues.  While
-      // lane 0 is in the main loop the others bring the adapters' rows to L2.
+      // The whole warp walks the list, lane 0 issues.
       AdapterWindow win;
-      const MultiTile t = multi_open(p.multi, m_tile, win, [&](int a) {
-        prefetch_adapter(p.multi, C::B_MN, a, static_cast<int64_t>(n_tile) * C::BN, C::BN, p.out_cols);
-      });
+      MultiTile t{};
+      int ok = multi_open(p.multi, m_tile, list, p.err, &t) && __shfl_sync(0xffffffffu, issued, 0) == n_iters;
       const MultiSteps steps(p.multi, t);
       int lo, hi;
       steps.share(&lo, &hi);
-      int ok = __shfl_sync(0xffffffffu, issued, 0) == n_iters;
+      griddep_wait();      // the copies of T or U; the list is there, so the projection is done
       MultiStep at(steps, lo);
       for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
@@ -319,13 +321,14 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
     }
     if constexpr (C::MULTI) {
       MaskWindow<1> win;
-      const MultiTile t = multi_open(p.multi, m_tile, win, [](int) {});
+      MultiTile t{};
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = multi_open(p.multi, m_tile, list, p.err, &t) && ok;
       const MultiSteps steps(p.multi, t);
       const uint32_t w = 1u << steps.lw;
       int lo, hi;
       steps.share(&lo, &hi);
       MultiStep at(steps, lo);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
         const uint32_t ph = static_cast<uint32_t>(li / C::STAGES) & 1u;
@@ -356,6 +359,11 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
     if (lane == 0) {
       if (ok) umma_commit(&acc_bar);
     }
+  } else if (C::MULTI && warp == 2 + C::NUM_EPI_WARPS) {
+    if constexpr (C::MULTI)
+      multi_scout(p.multi, m_tile, list, [&](int a) {
+        prefetch_adapter(p.multi, C::B_MN, a, static_cast<int64_t>(n_tile) * C::BN, C::BN, p.out_cols);
+      });
   } else {
     // ------------------------------------------------------------ dequant
     // Groups of 8 warps take k-steps in turn, so DQ_GROUPS B tiles are being
@@ -402,23 +410,10 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       // group count), so that a group waits on every phase of its stages'
       // barriers and a parity wait cannot be satisfied by an older phase.
       static_assert(C::DQ_GROUPS <= 1 || C::STAGES % C::DQ_GROUPS == 0, "stages per dequant group");
-      // Many adapters: the tile's list is requested two of the group's steps
-      // before the main loop ends.
-      AdapterWindow win;
-      int adapters = -1;
-      const auto open_list = [&]() {
-        if (adapters >= 0) return;
-        griddep_wait();
-        adapters = __ldcg(multi_tile_at(p.multi, m_tile));
-        win.prime(p.multi, multi_tile_at(p.multi, m_tile));
-      };
       for (int li = grp; li < n_iters; li += kStride) {
         const int it = it_begin + li;
         const int s = li % C::STAGES;
         const uint32_t ph = static_cast<uint32_t>(li / C::STAGES) & 1u;
-        if constexpr (C::MULTI && !C::B_MN) {
-          if (li + 2 * kStride >= n_iters) open_list();
-        }
         if (!mbar_wait_bounded(&full_a[s], ph, p.err, kErrTimeoutFullA)) { ok = false; break; }
         if (it < p.num_main) {
           const int64_t blk = blk_nx;
@@ -465,9 +460,10 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       if constexpr (C::MULTI && !C::B_MN) {
         // The adapter k-steps' rows of B_a, requested a step of the group
         // ahead.
-        if (__all_sync(0xffffffffu, ok)) {
-          open_list();
-          const MultiTile t = multi_tile_of(p.multi, multi_tile_at(p.multi, m_tile), adapters);
+        MultiTile t{};
+        ok = __all_sync(0xffffffffu, ok) && multi_open(p.multi, m_tile, list, p.err, &t);
+        if (ok) {
+          AdapterWindow win;
           const MultiSteps steps(p.multi, t);
           int lo, hi;
           steps.share(&lo, &hi);
@@ -693,7 +689,7 @@ int choose_split(int64_t tiles, int ksteps, int per_sm) {
 }
 
 int ClusterFit::split(const void *kernel, int threads, int smem_bytes, int64_t tiles, int per_sm, int most_split,
-                      int *clusters) {
+                      int *clusters, int most_sms) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   const bool slot = dev >= 0 && dev < kMaxDevicesPerProcess;
@@ -719,6 +715,7 @@ int ClusterFit::split(const void *kernel, int threads, int smem_bytes, int64_t t
       }
       if (slot) resident[dev][s].store(n, std::memory_order_relaxed);
     }
+    if (n > most_sms / s) n = s == 1 || s % 2 == 0 ? most_sms / s : 0;
     *clusters = n * per_sm;
     if (n * per_sm >= tiles || s == 1) return s;
   }
@@ -809,6 +806,14 @@ int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps) {
   if (pair_ctas > 74 || tiles > 148) return 512;
   const int sp = choose_split(tiles, static_cast<int>(ksteps), 1);
   return 85 * (ksteps + sp - 1) / sp < 55 * ksteps ? 128 : 512;
+}
+
+MultiGrid multi_grid(int64_t m, int64_t cols, int64_t ksteps, int rows) {
+  const int64_t gn = (cols + 255) / 256;
+  if (rows != 128) return MultiGrid{2 * gn * ((m + 511) / 512), ksteps};
+  const int64_t tiles = gn * ((m + 127) / 128);
+  const int sp = choose_split(tiles, static_cast<int>(ksteps), 1);
+  return MultiGrid{tiles * sp, ksteps / sp};
 }
 
 cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,

@@ -27,11 +27,15 @@ WORKLOADS = {
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", choices=("quantize", "quantize_fp8", "dequant", "fwd", "fwd_nolora", "bwd_dx", "lora_bwd",
-                                     "merge", "dropout", "fwd_dropout", "bwd_dx_dropout"), required=True)
+                                     "merge", "dropout", "fwd_dropout", "bwd_dx_dropout", "act_quantize",
+                                     "act_dequant", "bwd_act8", "fwd_multi", "bwd_multi"), required=True)
     ap.add_argument("--workload", choices=sorted(WORKLOADS), required=True)
     ap.add_argument("--m", type=int, default=4096)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--warmup", type=int, default=2)
+    ap.add_argument("--adapters", type=int, default=8, help="adapters of fwd_multi and bwd_multi")
+    ap.add_argument("--rows", choices=("runs", "mixed"), default="runs",
+                    help="their rows: each adapter's together, or in any order")
     a = ap.parse_args(argv)
 
     dev = torch.device("cuda", 0)
@@ -44,20 +48,42 @@ def main(argv=None):
         del W
     r = case.r
     X = A = Bm = dY = Y = None
-    if a.op in ("fwd", "fwd_nolora", "lora_bwd", "dropout", "fwd_dropout"):
+    if a.op in ("fwd", "fwd_nolora", "lora_bwd", "dropout", "fwd_dropout", "act_quantize", "act_dequant", "bwd_act8",
+                "fwd_multi", "bwd_multi"):
         X = case.X().to(dev)
-    if a.op in ("bwd_dx", "lora_bwd", "bwd_dx_dropout"):
+    if a.op in ("bwd_dx", "lora_bwd", "bwd_dx_dropout", "bwd_act8", "bwd_multi"):
         dY = case.dY().to(dev)
     A, Bm = case.A().to(dev), case.B().to(dev)
     out_w = torch.empty(case.n, case.k, dtype=torch.bfloat16, device=dev) if a.op in ("dequant", "merge") else None
-    if a.op in ("fwd", "fwd_nolora", "fwd_dropout"):
+    if a.op in ("fwd", "fwd_nolora", "fwd_dropout", "fwd_multi"):
         Y = torch.empty(case.m, case.n, dtype=torch.bfloat16, device=dev)
     Xd = torch.empty_like(X) if a.op in ("dropout", "fwd_dropout") else None
     if a.op in ("bwd_dx", "bwd_dx_dropout"):
         Y = torch.empty(case.m, case.k, dtype=torch.bfloat16, device=dev)
+    act = T = As = Bs = scales = ids = None
+    if a.op in ("act_quantize", "act_dequant", "bwd_act8"):
+        act = B.qlora_act_quantize(X)
+    if a.op in ("bwd_act8", "bwd_multi"):
+        T = WL.bf16(WL.normal((case.m, r), 1.0, 3)).to(dev)
+    if a.op in ("fwd_multi", "bwd_multi"):
+        As, Bs = A.repeat(a.adapters, 1, 1), Bm.repeat(a.adapters, 1, 1)
+        scales = torch.full((a.adapters,), case.scale, device=dev)
+        ids = torch.arange(case.m, dtype=torch.int32, device=dev)
+        ids = ids * a.adapters // case.m if a.rows == "runs" else ids * 7 % a.adapters
+        ids = ids.to(torch.int32)
 
     def run():
-        if a.op == "quantize":
+        if a.op == "act_quantize":
+            B.qlora_act_quantize(X, out=act)
+        elif a.op == "act_dequant":
+            B.qlora_act_dequant(act, out=X)
+        elif a.op == "bwd_act8":
+            B.qlora_linear_bwd_act8(dY, act, w, A, Bm, r, case.scale, T)
+        elif a.op == "fwd_multi":
+            B.qlora_linear_fwd_multi(X, w, As, Bs, scales, ids, out=Y)
+        elif a.op == "bwd_multi":
+            B.qlora_linear_bwd_multi(dY, X, w, As, Bs, scales, ids, T=T)
+        elif a.op == "quantize":
             B.qlora_quantize_nf4_dq(W, out=w)
         elif a.op == "quantize_fp8":
             B.qlora_quantize_4bit_dq(W, B.QLORA_CODEBOOK_NF4, out=w8, dq_format=B.QLORA_DQ_FP8_MEAN)
