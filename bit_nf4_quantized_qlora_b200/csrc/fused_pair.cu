@@ -203,40 +203,42 @@ __global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_ker
       // Adapter k-steps of the tile's list.  This CTA's rows of a rank block
       // of T or U go into each activation slot once; the input gradient's
       // adapter rows come by TMA, the forward's from the dequant warps.  The
-      // whole warp walks the list, lane 0 issues.
-      AdapterWindow win;
+      // whole warp walks the units, lane 0 issues.
+      UnitWindow win;
       MultiTile t{};
-      int ok = multi_open(p.multi, m_pair, list, p.err, &t) && __shfl_sync(0xffffffffu, issued, 0) == total;
+      int ok = multi_open(p.multi, m_pair, list, p.err, &t);
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      ok = ok && issued == total;
       const MultiSteps steps(p.multi, t);
       griddep_wait();      // the copies of T or U; the list is there, so the projection is done
       const int n_steps = steps.count();
-      MultiStep at(steps, 0);
-      for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
+      for (int st = 0; st < n_steps && ok; ++st) {
         const int it = total + st, s = it % kStages;
         const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
         const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
         const uint32_t xbar = mapa_shared(smem_u32(&xfull[s]), 0);
-        MultiStep step = at;
-        const bool fresh = step.since < kStages;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(it / kStages) & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
-          if (ok) {
-            if (leader)
-              mbar_arrive_expect_tx(&xfull[s], 2u * ((fresh ? kABytes : 0u) +
-                                                     (BWD ? (static_cast<uint32_t>(step.units) << steps.lw) * 256u : 0u)));
+        const int g = st << steps.lp, units = steps.units_of(st);
+        const bool fresh = steps.since(st, 0) < kStages;
+        win.move(t, steps, g);
+        const int block = win.col_of(g) >> 6;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(it / kStages) & 1u) ^ 1u, p.err,
+                                                       kErrTimeoutEmpty));
+        if (!ok) break;
+        if (elect_lane()) {
+          if (leader)
+            mbar_arrive_expect_tx(&xfull[s], 2u * ((fresh ? kABytes : 0u) +
+                                                   (BWD ? (static_cast<uint32_t>(units) << steps.lw) * 256u : 0u)));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int y = (m0 + h * 128 < p.m) ? m0 + h * 128 : 0;
-              if (fresh) tma_load_2d_pair(xa + h * kASub, &p.tmA2, xbar, step.block * kBK, y);
-            }
-            ++issued;
+          for (int h = 0; h < 2; ++h) {
+            const int y = (m0 + h * 128 < p.m) ? m0 + h * 128 : 0;
+            if (fresh) tma_load_2d_pair(xa + h * kASub, &p.tmA2, xbar, block * kBK, y);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++issued;
         if (BWD) {
-          for (int u = 0; u < step.units; ++u, step.advance()) {
-            const int a = win.at(t, step.slot), c = step.block * 64 + (step.sub << steps.lw);
-            if (lane == 0 && ok) {
+          for (int u = 0; u < units; ++u) {
+            const int a = win.id_of(g + u), c = win.col_of(g + u);
+            if (elect_lane()) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const int64_t col = c0 + 64 * j;
@@ -314,38 +316,42 @@ __global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_ker
         const MultiSteps steps(p.multi, t);
         const uint32_t w = 1u << steps.lw;
         const int n_steps = steps.count();
-        MultiStep at(steps, 0);
-        for (int st = 0; st < n_steps && ok; ++st, at.next(steps)) {
+        for (int st = 0; st < n_steps && ok; ++st) {
           const int it = total + st, s = it % kStages;
           const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1u;
           const uint32_t xa = base + static_cast<uint32_t>(s) * kABytes;
           const uint32_t wb = base + kBRing + static_cast<uint32_t>(s) * kBBytes;
-          if (lane == 0) {
-            ok = mbar_wait_cluster_bounded(&xfull[s], ph, p.err, kErrTimeoutFullA);
-            if (ok && !BWD) ok = mbar_wait_cluster_bounded(&wfull[s], ph, p.err, kErrTimeoutFullB);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          ok = mbar_wait_cluster_bounded(&xfull[s], ph, p.err, kErrTimeoutFullA);
+          if (ok && !BWD) ok = mbar_wait_cluster_bounded(&wfull[s], ph, p.err, kErrTimeoutFullB);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) tc_fence_after();
-          MultiStep step = at;
+          tc_fence_after();
+          const int g = st << steps.lp, units = steps.units_of(st);
           const uint64_t ad = smem_desc(xa, 16u, 1024u);
           const uint64_t bd = BWD ? smem_desc(wb, 8192u, 1024u) : smem_desc_unit(wb, 16u, 16u * w, static_cast<int>(w));
-          for (int u = 0; u < step.units; ++u, step.advance()) {
-            win.load(t, step.slot);
-            if (lane == 0) {
-              // Offsets in the descriptors' 16-byte units.
-              const uint64_t ua = ad + ((static_cast<uint32_t>(step.sub) << steps.lw) >> 3);
-              const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (BWD ? 8u : 16u);
+          for (int u = 0; u < units; ++u) {
+            win.take(t, steps, g + u);
+            // Offsets in the descriptors' 16-byte units.
+            const uint64_t ua = ad + (static_cast<uint32_t>(win.col_of(g + u) & 63) >> 3);
+            const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (BWD ? 8u : 16u);
+            if (elect_lane()) {
 #pragma unroll
               for (uint32_t h = 0; h < 2; ++h) {
                 // Rows 128 h .. of the even CTA's 256, then of the odd CTA's.
-                for (uint32_t kk = 0; kk < w / 16u; ++kk)
+                const auto product = [&](uint32_t kk) {
                   umma_f16_pair_masked(tmem + h * kBN, ua + h * (kASub / 16u) + kk * 2u, ub + kk * (BWD ? 128u : 2u),
                                        kIdesc, win.off[h], win.off[2 + h]);
+                };
+                product(0);
+                if (w > 16u) product(1);
+                if (w > 32u) {
+                  product(2);
+                  product(3);
+                }
               }
             }
           }
-          if (lane == 0) umma_commit_pair_both(&empty[s]);
+          if (elect_lane()) umma_commit_pair_both(&empty[s]);
         }
       }
     }
@@ -353,8 +359,7 @@ __global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_ker
       if (ok) umma_commit_pair_both(&acc_full);
     }
   } else if (MULTI && warp == kScoutWarp) {
-    if constexpr (MULTI)
-      multi_scout(p.multi, m_pair, list, [&](int a) { prefetch_adapter(p.multi, BWD, a, c0, kHalfN, p.out_cols); });
+    if constexpr (MULTI) multi_scout(p.multi, m_pair, list);
   } else {
     // ------------------------------------------------------------ dequant
     const int dq = warp - kFirstDqWarp;
@@ -454,27 +459,25 @@ __global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_ker
     if constexpr (MULTI && !BWD) {
       // The adapter k-steps' rows of B_a (this CTA's half tile), requested a
       // step of the group ahead.
-      AdapterWindow win;
       MultiTile t{};
-      const bool listed = multi_open(p.multi, m_pair, list, p.err, &t);
-      const MultiSteps steps(p.multi, t);
-      const int n_steps = listed ? steps.count() : 0;
-      int st = ((grp - total % kGroups) + kGroups) % kGroups;
-      MultiStep at(steps, 0);
-      for (int i = 0; i < st; ++i) at.next(steps);
-      MultiRows<kHalfN> rows;
-      if (st < n_steps) rows.load(p.multi, at, win, t, p.n, c0, dt);
-      for (; st < n_steps; st += kGroups) {
-        const uint32_t use = static_cast<uint32_t>((total + st) / kStages);
-        const bool free_slot = mbar_wait_bounded(&empty[grp], (use & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
-        if (!__all_sync(0xffffffffu, free_slot)) break;
-        rows.store(p.multi, wslot, dt);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(wbar);
-        for (int i = 0; i < kGroups; ++i) at.next(steps);
-        if (st + kGroups < n_steps) rows.load(p.multi, at, win, t, p.n, c0, dt);
-      }
+      const auto fill = [&](auto width) {
+        const MultiSteps steps(p.multi, t);
+        const int n_steps = steps.count();
+        int st = ((grp - total % kGroups) + kGroups) % kGroups;
+        MultiRows<kHalfN, decltype(width)::value> rows(p.multi, p.n, c0, dt);
+        if (st < n_steps) rows.load(p.multi, t, steps, st, p.n, c0, dt);
+        for (; st < n_steps; st += kGroups) {
+          const uint32_t use = static_cast<uint32_t>((total + st) / kStages);
+          const bool free_slot = mbar_wait_bounded(&empty[grp], (use & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
+          if (!__all_sync(0xffffffffu, free_slot)) break;
+          rows.store(wslot);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(wbar);
+          if (st + kGroups < n_steps) rows.load(p.multi, t, steps, st + kGroups, p.n, c0, dt);
+        }
+      };
+      if (multi_open(p.multi, m_pair, list, p.err, &t)) by_width(p.multi.width, fill);
     }
 
     // ------------------------------------------------------------ epilogue

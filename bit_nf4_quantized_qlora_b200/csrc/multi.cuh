@@ -16,6 +16,8 @@
 // width, in atoms of 8 rows.
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -107,6 +109,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp, the same at every call.  Copies and products
+// are issued under it: their operands live in warp-wide registers, and under a
+// test of the lane's number the compiler moves each of them through a loop over
+// the lanes (a masked product took 600 cycles to issue, 100 under this).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0u;
+}
+
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -147,12 +159,10 @@ __device__ __forceinline__ const int32_t *multi_tile_at(const MultiParams &p, in
 
 // The warp of a kernel that overlaps the projection, for all of its others:
 // waits for the projection (which stops a whole warp, so no warp of the main
-// loop may), takes the list and passes its adapters to `prefetch`, whose rows
-// are in L2 when the main loop ends.  Reads past L1: the lists were written
-// while this kernel ran.
-template <int QUADS, class Prefetch>
-__device__ __forceinline__ void multi_scout(const MultiParams &p, int tile, MultiListSmem<QUADS> &s,
-                                            const Prefetch &prefetch) {
+// loop may) and takes the list.  Reads past L1: it was written while this
+// kernel ran.
+template <int QUADS>
+__device__ __forceinline__ void multi_scout(const MultiParams &p, int tile, MultiListSmem<QUADS> &s) {
   griddep_wait();
   const int32_t *t = multi_tile_at(p, tile);
   const uint4 *mask = reinterpret_cast<const uint4 *>(t + 4 + p.slots);
@@ -165,7 +175,6 @@ __device__ __forceinline__ void multi_scout(const MultiParams &p, int tile, Mult
   if (lane == 0) s.adapters = n;
   __syncwarp();
   if (lane == 0) mbar_arrive(&s.ready);
-  for (int i = lane; i < n; i += 32) prefetch(__ldcg(t + 4 + i));
 }
 // The list in one of the other warps; false if the wait for it ran out.
 template <int QUADS>
@@ -178,77 +187,29 @@ __device__ __forceinline__ bool multi_open(const MultiParams &p, int tile, Multi
   return true;
 }
 
-// A warp's window on the list, so that the latency of a list read is paid once
-// per 32 adapters: entry first + i is in lane i.  Called by whole warps.
-struct AdapterWindow {
-  int first = -32, id = 0;
-  __device__ __forceinline__ int at(const MultiTile &t, int slot) {
-    if (slot < first || slot >= first + 32) {
-      first = slot & ~31;
-      const int i = first + static_cast<int>(lane_id());
-      id = i >= t.adapters ? 0 : i < kListEntries ? t.id_smem[i] : __ldcg(t.list + i);
-    }
-    return __shfl_sync(0xffffffffu, id, slot - first);
-  }
-};
-// Likewise the row masks; off[q] is the lane mask of rows 128 q .. of the
-// tile: set where the row is not the adapter's.
-template <int QUADS>
-struct MaskWindow {
-  int first = -32, current = -1;
-  uint4 on[QUADS];
-  uint4 off[QUADS];
-  __device__ __forceinline__ void load(const MultiTile &t, int slot) {
-    if (slot == current) return;
-    current = slot;
-    if (slot < first || slot >= first + 32) {
-      first = slot & ~31;
-      const int i = first + static_cast<int>(lane_id());
-#pragma unroll
-      for (int q = 0; q < QUADS; ++q)
-        on[q] = i >= t.adapters ? make_uint4(0u, 0u, 0u, 0u)
-                : i < kListEntries ? t.mask_smem[i * QUADS + q]
-                                   : __ldcg(t.mask + i * QUADS + q);
-    }
-    const int l = slot - first;
-#pragma unroll
-    for (int q = 0; q < QUADS; ++q)
-      off[q] = make_uint4(~__shfl_sync(0xffffffffu, on[q].x, l), ~__shfl_sync(0xffffffffu, on[q].y, l),
-                          ~__shfl_sync(0xffffffffu, on[q].z, l), ~__shfl_sync(0xffffffffu, on[q].w, l));
-  }
-};
-
-// `bytes` (a multiple of 16) at `src` into L2.
-__device__ __forceinline__ void prefetch_l2(const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-// An adapter's part of an output tile: rows [c0, c0 + cols) of B_a (forward),
-// or columns [c0, c0 + cols) of A_a's r rows.
-__device__ __forceinline__ void prefetch_adapter(const MultiParams &p, bool bwd, int64_t a, int64_t c0, int cols,
-                                                 int64_t out_cols) {
-  const int64_t left = out_cols - c0;
-  if (left <= 0) return;
-  const uint32_t c = static_cast<uint32_t>(left < cols ? left : cols);
-  if (!bwd) {
-    prefetch_l2(p.B + (a * out_cols + c0) * p.r, c * static_cast<uint32_t>(p.r) * 2u);
-  } else {
-    for (int j = 0; j < p.r; ++j) prefetch_l2(p.A + (a * p.r + j) * out_cols + c0, c * 2u);
-  }
-}
-
 // The adapter k-steps of a tile, block by block of the rank: every full
 // 64-column block has one step per adapter, the last partial block packs
-// 64 / width units into each.  A walk over them keeps its place in counters:
-// the warps that issue products have one instruction in flight at a time, and a
-// division would cost them as much as a step's products.
+// 64 / w units into each.  Units are numbered in that order, so unit g is part
+// g % (64 / w) of step g / (64 / w).
 struct MultiSteps {
-  int adapters, full, rest;            // full 64-column blocks; columns of the partial one
-  int lw;                              // log2 of the unit width
-  int per_step;                        // 64 / width
+  int adapters, full, rest;            // full 64-column blocks; units of an adapter in the partial one
+  int lw, lp;                          // log2 of the unit width; of the units of a step
+  int units;
   __device__ __forceinline__ MultiSteps(const MultiParams &p, const MultiTile &t)
-      : adapters(t.adapters), full(p.r >> 6), rest(p.r & 63), lw(p.width == 64 ? 6 : p.width == 32 ? 5 : 4),
-        per_step(64 >> lw) {}
-  __device__ __forceinline__ int count() const { return full * adapters + ((adapters * rest + 63) >> 6); }
+      : adapters(t.adapters), full(p.r >> 6), lw(p.width == 64 ? 6 : p.width == 32 ? 5 : 4), lp(6 - lw) {
+    rest = (p.r & 63) >> lw;
+    units = t.adapters * (p.r >> lw);
+  }
+  __device__ __forceinline__ int count() const { return (units + (1 << lp) - 1) >> lp; }
+  __device__ __forceinline__ int units_of(int step) const {
+    const int left = units - (step << lp);
+    return left < 1 << lp ? left : 1 << lp;
+  }
+  // Steps of the walk that starts at `lo` before `step` in its rank block.
+  __device__ __forceinline__ int since(int step, int lo) const {
+    int first = step < full * adapters ? step - step % adapters : full * adapters;
+    return step - (first < lo ? lo : first);
+  }
   // This CTA's share [lo, hi) along a cluster's z.
   __device__ __forceinline__ void share(int *lo, int *hi) const {
     const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
@@ -256,116 +217,114 @@ struct MultiSteps {
     *hi = static_cast<int>((static_cast<int64_t>(count()) * (z + 1)) / nz);
   }
 };
-struct MultiStep {
-  int block, units, per_adapter;          // rank block; units of the step, units of an adapter in the block
-  int slot, sub;                          // adapter and unit of the step's first
-  int left;                               // units of the block from this step on
-  int since;                              // steps of the walk in this block
-  // The step `st` of a walk that starts there.
-  __device__ __forceinline__ MultiStep(const MultiSteps &s, int st) {
-    const int in_full = s.full * s.adapters;
-    block = 0;
-    int at = st;
-    while (block < s.full && at >= s.adapters && s.adapters > 0) {
-      at -= s.adapters;
-      ++block;
+
+// A warp's window of 32 units: unit first + i is worked out by lane i.  The
+// warps that issue copies and products run one instruction chain each, and a
+// walk through the units with its divisions and list reads took them three
+// times a main loop's k-step; a window's 32 units cost about as much as one.
+struct UnitWindow {
+  int first = -32, slot = 0, id = 0, col = 0;      // list entry, adapter, rank column
+  // Whole warps; true if the window moved to unit g.
+  __device__ __forceinline__ bool move(const MultiTile &t, const MultiSteps &s, int g) {
+    if ((g & ~31) == first) return false;
+    first = g & ~31;
+    const int i = first + static_cast<int>(lane_id()), in_full = (s.full * s.adapters) << s.lp;
+    int block, sub;
+    if (i < in_full) {
+      const int step = i >> s.lp;
+      block = step / s.adapters;
+      slot = step - block * s.adapters;
+      sub = i & ((1 << s.lp) - 1);
+    } else {
+      const int per = s.rest > 0 ? s.rest : 1;
+      block = s.full;
+      slot = (i - in_full) / per;
+      sub = i - in_full - slot * per;
     }
-    if (st >= in_full) block = s.full;
-    open(s);
-    sub += at * s.per_step;
-    left -= sub;
-    slot = sub / per_adapter;
-    sub -= slot * per_adapter;
-    units = left < s.per_step ? left : s.per_step;
+    if (i >= s.units) slot = 0;
+    id = slot < kListEntries ? t.id_smem[slot] : __ldcg(t.list + slot);
+    col = block * 64 + (sub << s.lw);
+    return true;
   }
-  __device__ __forceinline__ void open(const MultiSteps &s) {
-    per_adapter = block < s.full ? s.per_step : (s.rest >> s.lw);
-    if (per_adapter == 0) per_adapter = 1;       // past the last block
-    left = s.adapters * per_adapter;
-    slot = sub = since = 0;
-    units = left < s.per_step ? left : s.per_step;
-  }
-  // To the walk's next step.
-  __device__ __forceinline__ void next(const MultiSteps &s) {
-    left -= units;
-    ++since;
-    if (left == 0) {
-      ++block;
-      open(s);
-      return;
+  __device__ __forceinline__ int id_of(int g) const { return __shfl_sync(0xffffffffu, id, g & 31); }
+  __device__ __forceinline__ int col_of(int g) const { return __shfl_sync(0xffffffffu, col, g & 31); }
+};
+// With the lane masks of QUADS * 128 rows: off[q] of rows 128 q .. of the
+// tile, set where the row is not the unit's adapter's.
+template <int QUADS>
+struct MaskWindow : UnitWindow {
+  uint4 all[QUADS], off[QUADS];
+  __device__ __forceinline__ void take(const MultiTile &t, const MultiSteps &s, int g) {
+    if (move(t, s, g)) {
+#pragma unroll
+      for (int q = 0; q < QUADS; ++q) {
+        const uint4 on = slot < kListEntries ? t.mask_smem[slot * QUADS + q] : __ldcg(t.mask + slot * QUADS + q);
+        all[q] = make_uint4(~on.x, ~on.y, ~on.z, ~on.w);
+      }
     }
-    sub += units;
-    while (sub >= per_adapter) {
-      sub -= per_adapter;
-      ++slot;
-    }
-    units = left < s.per_step ? left : s.per_step;
-  }
-  // To the step's next unit (of a copy).
-  __device__ __forceinline__ void advance() {
-    if (++sub == per_adapter) {
-      sub = 0;
-      ++slot;
-    }
+#pragma unroll
+    for (int q = 0; q < QUADS; ++q)
+      off[q] = make_uint4(__shfl_sync(0xffffffffu, all[q].x, g & 31), __shfl_sync(0xffffffffu, all[q].y, g & 31),
+                          __shfl_sync(0xffffffffu, all[q].z, g & 31), __shfl_sync(0xffffffffu, all[q].w, g & 31));
   }
 };
 
+// f(integral_constant<int, unit width>).
+template <class F>
+__device__ __forceinline__ void by_width(int width, const F &f) {
+  if (width == 16)
+    f(std::integral_constant<int, 16>{});
+  else if (width == 32)
+    f(std::integral_constant<int, 32>{});
+  else
+    f(std::integral_constant<int, 64>{});
+}
+
 // A thread's part of a step's K-major adapter tile [ROWS x 64], ROWS threads:
 // 8 pieces of 16 bytes, taken from the matrices B_a [n x r] of the step's
-// adapters and stored as 64 / w units of ROWS rows under the unit's swizzle.
-// Plain loads, consecutive lanes on consecutive bytes: a unit row of 32 or 64
-// bytes would cost the copy engine as much as one of 128 (bulk copies of whole
-// adapters put in order in shared memory, and boxes for the 128-byte rows, took
-// the same time).
-template <int ROWS>
+// units of W columns and stored as 64 / W tiles of ROWS rows under the
+// swizzle of their width.  Plain loads, consecutive lanes on consecutive
+// bytes: a unit row of 32 or 64 bytes would cost the copy engine as much as
+// one of 128.  Rows past n and units past the step's keep what the registers
+// held; they meet no stored column and no product.
+template <int ROWS, int W>
 struct MultiRows {
+  static constexpr int kPieces = W / 8;             // of a unit row
+  static constexpr int kRowStep = ROWS / kPieces;   // rows between a thread's pieces (a multiple of 8)
+  UnitWindow win;
+  const uint16_t *src = nullptr;                    // the lane's unit, from row n0
+  uint32_t dst;                                     // of piece 0 in the tile; piece q follows at 16 ROWS q
+  int row, left, r;
   uint4 v[8];
-  template <int W, class Window>
-  __device__ __forceinline__ void load_w(const MultiParams &p, MultiStep s, Window &win, const MultiTile &t, int64_t n,
-                                         int64_t n0, int thread) {
-    constexpr int kPieces = W / 8;      // of a unit row
+  __device__ __forceinline__ MultiRows(const MultiParams &p, int64_t n, int64_t n0, int thread)
+      : row(thread / kPieces), left(n - n0 < ROWS ? static_cast<int>(n - n0) : ROWS), r(p.r) {
+    const int piece = thread % kPieces, sw = (row >> (W == 64 ? 0 : W == 32 ? 1 : 2)) & (kPieces - 1);
+    dst = static_cast<uint32_t>(row * W * 2 + ((piece ^ sw) << 4));
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void load(const MultiParams &p, const MultiTile &t, const MultiSteps &s, int step,
+                                       int64_t n, int64_t n0, int thread) {
+    const int g = step * (64 / W), units = s.units_of(step);
+    if (win.move(t, s, g)) src = p.B + (win.id * n + n0) * r + win.col;
+    const int mine = row * r + (thread % kPieces) * 8;
 #pragma unroll
     for (int u = 0; u < 64 / W; ++u) {
-      const int a = u < s.units ? win.at(t, s.slot) : 0;
-      const uint16_t *src = p.B + (a * n + n0) * p.r + s.block * 64 + s.sub * W;
+      const uint16_t *from =
+          reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), (g + u) & 31)) +
+          mine;
 #pragma unroll
-      for (int c = 0; c < kPieces; ++c) {
-        const int j = c * ROWS + thread, row = j / kPieces;
-        v[u * kPieces + c] = u < s.units && n0 + row < n
-                                 ? __ldg(reinterpret_cast<const uint4 *>(src + row * p.r) + j % kPieces)
-                                 : make_uint4(0u, 0u, 0u, 0u);
-      }
-      s.advance();
+      for (int c = 0; c < kPieces; ++c)
+        if (u < units && row + c * kRowStep < left)
+          v[u * kPieces + c] = __ldg(reinterpret_cast<const uint4 *>(from + c * kRowStep * r));
     }
   }
-  template <class Window>
-  __device__ __forceinline__ void load(const MultiParams &p, const MultiStep &s, Window &win, const MultiTile &t,
-                                       int64_t n, int64_t n0, int thread) {
-    if (p.width == 16)
-      load_w<16>(p, s, win, t, n, n0, thread);
-    else if (p.width == 32)
-      load_w<32>(p, s, win, t, n, n0, thread);
-    else
-      load_w<64>(p, s, win, t, n, n0, thread);
-  }
-  template <int W>
-  __device__ __forceinline__ void store_w(uint32_t tile, int thread) const {
-    constexpr int kPieces = W / 8;
+  __device__ __forceinline__ void store(uint32_t tile) const {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int j = (q % kPieces) * ROWS + thread, row = j / kPieces;
-      const int sw = (row >> (W == 64 ? 0 : W == 32 ? 1 : 2)) & (kPieces - 1);
       const uint32_t o[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-      sts128(tile + static_cast<uint32_t>(((q / kPieces) * ROWS + row) * W * 2 + (((j % kPieces) ^ sw) << 4)), o);
+      sts128(tile + dst + static_cast<uint32_t>(q) * (16u * ROWS), o);
     }
-  }
-  __device__ __forceinline__ void store(const MultiParams &p, uint32_t tile, int thread) const {
-    if (p.width == 16)
-      store_w<16>(tile, thread);
-    else if (p.width == 32)
-      store_w<32>(tile, thread);
-    else
-      store_w<64>(tile, thread);
   }
 };
 

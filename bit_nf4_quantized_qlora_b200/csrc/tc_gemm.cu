@@ -246,36 +246,36 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       // or U (from the preceding projection) goes into each stage once; the
       // input gradient's adapter rows come by TMA, the forward's from the
       // dequant warps.
-      // The whole warp walks the list, lane 0 issues.
-      AdapterWindow win;
+      // The whole warp walks the units, lane 0 issues.
+      UnitWindow win;
       MultiTile t{};
-      int ok = multi_open(p.multi, m_tile, list, p.err, &t) && __shfl_sync(0xffffffffu, issued, 0) == n_iters;
+      int ok = multi_open(p.multi, m_tile, list, p.err, &t);
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      ok = ok && issued == n_iters;
       const MultiSteps steps(p.multi, t);
       int lo, hi;
       steps.share(&lo, &hi);
       griddep_wait();      // the copies of T or U; the list is there, so the projection is done
-      MultiStep at(steps, lo);
-      for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
+      for (int st = lo; st < hi && ok; ++st) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
         const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
-        MultiStep step = at;
-        const bool fresh = step.since < C::STAGES;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u, p.err,
-                                 kErrTimeoutEmpty);
-          if (ok) {
-            mbar_arrive_expect_tx(&full_a[s],
-                                  (fresh ? C::A_BYTES : 0u) +
-                                      (C::B_MN ? (static_cast<uint32_t>(step.units) << steps.lw) * 2u * C::BN : 0u));
-            if (fresh) tma_load_2d(a_s, &p.tmA2, &full_a[s], step.block * kBK, m_tile * C::BM);
-            ++issued;
-          }
+        const int g = st << steps.lp, units = steps.units_of(st);
+        const bool fresh = steps.since(st, lo) < C::STAGES;
+        win.move(t, steps, g);
+        const int block = win.col_of(g) >> 6;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u,
+                                                       p.err, kErrTimeoutEmpty));
+        if (!ok) break;
+        if (elect_lane()) {
+          mbar_arrive_expect_tx(&full_a[s], (fresh ? C::A_BYTES : 0u) +
+                                                (C::B_MN ? (static_cast<uint32_t>(units) << steps.lw) * 2u * C::BN : 0u));
+          if (fresh) tma_load_2d(a_s, &p.tmA2, &full_a[s], block * kBK, m_tile * C::BM);
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++issued;
         if (C::B_MN) {
-          for (int u = 0; u < step.units; ++u, step.advance()) {
-            const int a = win.at(t, step.slot), c = step.block * 64 + (step.sub << steps.lw);
-            if (lane == 0 && ok) {
+          for (int u = 0; u < units; ++u) {
+            const int a = win.id_of(g + u), c = win.col_of(g + u);
+            if (elect_lane()) {
 #pragma unroll
               for (int j = 0; j < C::BN / 64; ++j)
                 tma_load_3d(b_s + j * 8192u + (static_cast<uint32_t>(u) << steps.lw) * 128u, &p.tmB2, &full_a[s],
@@ -328,42 +328,43 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
       const uint32_t w = 1u << steps.lw;
       int lo, hi;
       steps.share(&lo, &hi);
-      MultiStep at(steps, lo);
-      for (int st = lo; st < hi && ok; ++st, at.next(steps)) {
+      for (int st = lo; st < hi && ok; ++st) {
         const int li = n_iters + st - lo, s = li % C::STAGES;
         const uint32_t ph = static_cast<uint32_t>(li / C::STAGES) & 1u;
         const uint32_t a_s = base + static_cast<uint32_t>(s) * C::STAGE_BYTES, b_s = a_s + C::A_BYTES;
-        if (lane == 0) {
-          ok = mbar_wait_bounded(&full_a[s], ph, p.err, kErrTimeoutFullA);
-          if (ok && !C::B_MN) ok = mbar_wait_bounded(&full_b[s], ph, p.err, kErrTimeoutFullB);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = mbar_wait_bounded(&full_a[s], ph, p.err, kErrTimeoutFullA);
+        if (ok && !C::B_MN) ok = mbar_wait_bounded(&full_b[s], ph, p.err, kErrTimeoutFullB);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (lane == 0) tc_fence_after();
-        MultiStep step = at;
+        tc_fence_after();
+        const int g = st << steps.lp, units = steps.units_of(st);
         const uint64_t ad = smem_desc(a_s, 16u, 1024u);
         const uint64_t bd = C::B_MN ? smem_desc(b_s, 8192u, 1024u) : smem_desc_unit(b_s, 16u, 16u * w, static_cast<int>(w));
-        for (int u = 0; u < step.units; ++u, step.advance()) {
-          win.load(t, step.slot);
-          if (lane == 0) {
-            // Offsets in the descriptors' 16-byte units.
-            const uint64_t ua = ad + ((static_cast<uint32_t>(step.sub) << steps.lw) >> 3);
-            const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (C::B_MN ? 8u : 2u * C::BN / 16u);
-            for (uint32_t kk = 0; kk < w / 16u; ++kk)
+        for (int u = 0; u < units; ++u) {
+          win.take(t, steps, g + u);
+          // Offsets in the descriptors' 16-byte units.
+          const uint64_t ua = ad + (static_cast<uint32_t>(win.col_of(g + u) & 63) >> 3);
+          const uint64_t ub = bd + (static_cast<uint32_t>(u) << steps.lw) * (C::B_MN ? 8u : 2u * C::BN / 16u);
+          if (elect_lane()) {
+            const auto product = [&](uint32_t kk) {
               umma_f16_masked(tmem, ua + kk * 2u, ub + kk * (C::B_MN ? 128u : 2u), C::IDESC, win.off[0]);
+            };
+            product(0);
+            if (w > 16u) product(1);
+            if (w > 32u) {
+              product(2);
+              product(3);
+            }
           }
         }
-        if (lane == 0) umma_commit(&empty_bar[s]);
+        if (elect_lane()) umma_commit(&empty_bar[s]);
       }
     }
     if (lane == 0) {
       if (ok) umma_commit(&acc_bar);
     }
   } else if (C::MULTI && warp == 2 + C::NUM_EPI_WARPS) {
-    if constexpr (C::MULTI)
-      multi_scout(p.multi, m_tile, list, [&](int a) {
-        prefetch_adapter(p.multi, C::B_MN, a, static_cast<int64_t>(n_tile) * C::BN, C::BN, p.out_cols);
-      });
+    if constexpr (C::MULTI) multi_scout(p.multi, m_tile, list);
   } else {
     // ------------------------------------------------------------ dequant
     // Groups of 8 warps take k-steps in turn, so DQ_GROUPS B tiles are being
@@ -462,30 +463,27 @@ __global__ void __launch_bounds__(C::NUM_THREADS, 1) tc_kernel(const __grid_cons
         // ahead.
         MultiTile t{};
         ok = __all_sync(0xffffffffu, ok) && multi_open(p.multi, m_tile, list, p.err, &t);
-        if (ok) {
-          AdapterWindow win;
+        const auto fill = [&](auto width) {
           const MultiSteps steps(p.multi, t);
           int lo, hi;
           steps.share(&lo, &hi);
           const int64_t n0 = static_cast<int64_t>(n_tile) * C::BN;
           int st = lo + ((grp - n_iters % kStride) + kStride) % kStride;     // the group's first
-          MultiStep at(steps, lo);
-          for (int i = lo; i < st; ++i) at.next(steps);
-          MultiRows<C::BN> rows;
-          if (st < hi) rows.load(p.multi, at, win, t, p.w_n, n0, dt);
+          MultiRows<C::BN, decltype(width)::value> rows(p.multi, p.w_n, n0, dt);
+          if (st < hi) rows.load(p.multi, t, steps, st, p.w_n, n0, dt);
           for (; st < hi; st += kStride) {
             const int li = n_iters + st - lo, s = li % C::STAGES;
             ok = mbar_wait_bounded(&empty_bar[s], (static_cast<uint32_t>(li / C::STAGES) & 1u) ^ 1u, p.err,
                                    kErrTimeoutEmpty);
             if (!__all_sync(0xffffffffu, ok)) break;
-            rows.store(p.multi, base + static_cast<uint32_t>(s) * C::STAGE_BYTES + C::A_BYTES, dt);
+            rows.store(base + static_cast<uint32_t>(s) * C::STAGE_BYTES + C::A_BYTES);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full_b[s]);
-            for (int i = 0; i < kStride; ++i) at.next(steps);
-            if (st + kStride < hi) rows.load(p.multi, at, win, t, p.w_n, n0, dt);
+            if (st + kStride < hi) rows.load(p.multi, t, steps, st + kStride, p.w_n, n0, dt);
           }
-        }
+        };
+        if (ok) by_width(p.multi.width, fill);
       }
     }
 
