@@ -269,17 +269,15 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       const int want = first + 4 * lane;
       const bool in_order = idx.x == want && idx.y == want + 1 && idx.z == want + 2 && idx.w == want + 3;
       const bool box = __all_sync(0xffffffffu, lane >= 16 || in_order) != 0;
-      int ok = 1;
       const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
       const uint32_t r_s = l_s + kLBytes, c_s = r_s + kRBytes;
-      if (lane == 0) {
-        ok = mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u, p.err, kErrTimeoutEmpty);
-        if (ok) mbar_arrive_expect_tx(&full[s], (ACT8 ? kCBytes : kLBytes) + kRBytes);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      const int ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u,
+                                                               p.err, kErrTimeoutEmpty));
       if (!ok) break;
+      if (elect_lane()) mbar_arrive_expect_tx(&full[s], (ACT8 ? kCBytes : kLBytes) + kRBytes);
+      __syncwarp();
       if (box) {
-        if (lane == 0) {
+        if (elect_lane()) {
           if (ACT8) {
             tma_load_2d(c_s, &p.tmL, &full[s], p0, first);
           } else {
@@ -307,28 +305,28 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
         mbar_wait_bounded(&full[li % kStages], static_cast<uint32_t>(li / kStages) & 1u, p.err, kErrTimeoutDrain);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // Lane 0 issues; the warp meets only where a group ends (the walk, the
-    // zeroing of its last slot's pad rows).
     GroupWalk walk(p, lo, hi);
     Part part;
     int ok = 1, turn = 0, s = 0;
     uint32_t parity = 0u;
     const uint64_t ld0 = smem_desc(base, 8192u, 1024u), rd0 = smem_desc(base + kLBytes, 8192u, 1024u);
     const auto ready = [&]() {
-      return mbar_wait_bounded(&full[s], parity, p.err, kErrTimeoutFullA) &&
-             (!ACT8 || mbar_wait_bounded(&expanded[s], parity, p.err, kErrTimeoutFullB));
+      return __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], parity, p.err, kErrTimeoutFullA) &&
+                                         (!ACT8 || mbar_wait_bounded(&expanded[s], parity, p.err, kErrTimeoutFullB)));
     };
     // The products of 16 `chunks` rows of slot s.
     const auto multiply = [&](uint32_t acc, bool first, int chunks) {
       tc_fence_after();
       uint64_t ld = ld0 + static_cast<uint32_t>(s) * (kStageBytes >> 4), rd = rd0 + static_cast<uint32_t>(s) * (kStageBytes >> 4);
-      umma_f16(acc, ld, rd, kIdesc, first ? 0u : 1u);
-      for (int kk = 1; kk < chunks; ++kk) {
-        ld += 2048u / 16u;
-        rd += 2048u / 16u;
-        umma_f16(acc, ld, rd, kIdesc, 1u);
+      if (elect_lane()) {
+        umma_f16(acc, ld, rd, kIdesc, first ? 0u : 1u);
+        for (int kk = 1; kk < chunks; ++kk) {
+          ld += 2048u / 16u;
+          rd += 2048u / 16u;
+          umma_f16(acc, ld, rd, kIdesc, 1u);
+        }
+        umma_commit(&empty[s]);
       }
-      umma_commit(&empty[s]);
     };
     const auto advance = [&]() {
       if (++s == kStages) {
@@ -343,38 +341,32 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       // Whole slots, then (if it is in this share) a last one with pad rows.
       const int whole = p.list ? part.s + part.rows / kSlot : part.e;
       const int stop = whole < part.e ? whole : part.e;
-      if (lane == 0) {
-        if (!left)
-          ok = mbar_wait_bounded(&acc_empty[buf], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err, kErrTimeoutAcc);
-        for (int slot = part.b; slot < stop && ok; ++slot) {
-          ok = ready();
-          if (!ok) break;
-          multiply(acc, slot == part.b, kSlot / 16);
-          advance();
-        }
+      if (!left)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[buf], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err,
+                                                       kErrTimeoutAcc));
+      for (int slot = part.b; slot < stop && ok; ++slot) {
+        ok = ready();
+        if (!ok) break;
+        multiply(acc, slot == part.b, kSlot / 16);
+        advance();
       }
       if (!left) ++turn;
       if (stop < part.e) {
-        if (lane == 0) ok = ok && ready();
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = ok && ready();
         if (ok) {
           // Zero rows of R: whole 128-byte rows, so the swizzle inside them
           // does not matter.
-          const int at = __shfl_sync(0xffffffffu, s, 0);
           const int valid = part.rows % kSlot;
-          const uint32_t r_s = base + static_cast<uint32_t>(at) * kStageBytes + kLBytes;
+          const uint32_t r_s = base + static_cast<uint32_t>(s) * kStageBytes + kLBytes;
           const uint32_t zero[4] = {0u, 0u, 0u, 0u};
           for (int c = valid * 8 + lane; c < kSlot * 8; c += 32) sts128(r_s + static_cast<uint32_t>(c) * 16u, zero);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            multiply(acc, stop == part.b, (valid + 15) / 16);
-            advance();
-          }
+          multiply(acc, stop == part.b, (valid + 15) / 16);
+          advance();
         }
       }
-      if (lane == 0 && ok) umma_commit(&acc_full[buf]);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok && elect_lane()) umma_commit(&acc_full[buf]);
     }
   } else {
     const int t = static_cast<int>(threadIdx.x) - 64;

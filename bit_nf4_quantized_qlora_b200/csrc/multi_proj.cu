@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) multi_proj_kernel(const __grid_co
   __shared__ __align__(8) uint64_t acc_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int2 unit_list[kMaxCols / 16];
+  __shared__ const uint16_t *unit_src[kMaxCols / 16];
   __shared__ int key[256], first[256], list[kRows], slot_of[kRows], lead_slot[kRows], lead_count[4];
 
   __shared__ ListSmem lists_s;
@@ -315,30 +316,31 @@ __global__ void __launch_bounds__(kThreads, 1) multi_proj_kernel(const __grid_co
                               [] { named_barrier_sync(1, kListThreads); });
   }
 
+  if (warp == 0) issued = __shfl_sync(0xffffffffu, issued, 0);
   for (int pass = static_cast<int>(blockIdx.x); pass < passes; pass += p.pass_ctas) {
     const int a0 = pass * p.per_pass;                                       // the pass's adapters
     const int na = listed - a0 < p.per_pass ? listed - a0 : p.per_pass;
     const int nu = na * per_adapter;
     // The pass's units: adapter and first rank column.
     if (warp < 6) {
-      for (int u = threadIdx.x; u < nu; u += 192)
-        unit_list[u] = make_int2(list[a0 + u / per_adapter], (u % per_adapter) * w);
+      for (int u = threadIdx.x; u < nu; u += 192) {
+        const int id = list[a0 + u / per_adapter], c = (u % per_adapter) * w;
+        unit_list[u] = make_int2(id, c);
+        if (loaders) unit_src[u] = p.R + static_cast<int64_t>(id) * p.kc * p.r + c;
+      }
       named_barrier_sync(2, kThreads - kListThreads);
     }
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      if (lane == 0 && ok) {
-        for (int j = 0; j < steps; ++j) {
-          // The first pass's first copies of X are under way.
-          const bool fresh = pass != static_cast<int>(blockIdx.x) || j >= issued;
-          ok = mbar_wait_bounded(&empty[ring], parity ^ 1u, p.err, kErrTimeoutEmpty);
-          if (!ok) break;
+      for (int j = 0; j < steps && ok; ++j) {
+        // The first pass's first copies of X are under way.
+        const bool fresh = pass != static_cast<int>(blockIdx.x) || j >= issued;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[ring], parity ^ 1u, p.err, kErrTimeoutEmpty));
+        if (!ok) break;
+        if (elect_lane()) {
           mbar_arrive_expect_tx(&full[ring], static_cast<uint32_t>(p.tile_rows) * 128u +
                                                  (loaders ? 0u : static_cast<uint32_t>(nu) * unit_bytes));
-          if (fresh) {
-            load_x(ring, j);
-            ++issued;
-          }
+          if (fresh) load_x(ring, j);
           if (!loaders) {
             const uint32_t b_s = b_ring + static_cast<uint32_t>(ring) * b_bytes;
             for (int u = 0; u < nu; ++u) {
@@ -351,17 +353,18 @@ __global__ void __launch_bounds__(kThreads, 1) multi_proj_kernel(const __grid_co
                             unit.x);
             }
           }
-          if (++ring == stages) {
-            ring = 0;
-            parity ^= 1u;
-          }
+        }
+        if (fresh) ++issued;
+        if (++ring == stages) {
+          ring = 0;
+          parity ^= 1u;
         }
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0 && ok) {
-        // One thread issues everything, so what a step does not change is
-        // kept in registers: descriptors advance by additions (16-byte units).
+      if (ok) {
+        // What a step does not change is kept in registers: descriptors
+        // advance by additions (16-byte units).
         const uint32_t idesc = make_idesc(nu * w, false, R_MN);
         const uint64_t ad0 = smem_desc(base, 16u, 1024u);
         // MN-major units: [64 k-rows x w columns], one behind the other.
@@ -369,51 +372,51 @@ __global__ void __launch_bounds__(kThreads, 1) multi_proj_kernel(const __grid_co
                                   : smem_desc(b_ring, 16u, 1024u);
         const uint32_t b_step = R_MN ? static_cast<uint32_t>(2 * w) : 2u;
         for (int j = 0; j < steps; ++j) {
-          ok = mbar_wait_bounded(&full[ring], parity, p.err, kErrTimeoutFullA);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[ring], parity, p.err, kErrTimeoutFullA));
           if (!ok) break;
           tc_fence_after();
           uint64_t ad = ad0 + static_cast<uint32_t>(ring) * (kABytes >> 4);
           uint64_t bd = bd0 + static_cast<uint32_t>(ring) * (b_bytes >> 4);
-          umma_f16(tmem, ad, bd, idesc, j > 0 ? 1u : 0u);
+          if (elect_lane()) {
+            umma_f16(tmem, ad, bd, idesc, j > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 1; kk < kBK / 16; ++kk) {
-            ad += 2u;
-            bd += b_step;
-            umma_f16(tmem, ad, bd, idesc, 1u);
+            for (int kk = 1; kk < kBK / 16; ++kk) {
+              ad += 2u;
+              bd += b_step;
+              umma_f16(tmem, ad, bd, idesc, 1u);
+            }
+            umma_commit(&empty[ring]);
           }
-          umma_commit(&empty[ring]);
           if (++ring == stages) {
             ring = 0;
             parity ^= 1u;
           }
         }
-        if (ok) umma_commit(&acc_bar);
+        if (ok && elect_lane()) umma_commit(&acc_bar);
       }
     } else if (row_warp) {
       // ---------------------------------------------------------- adapter tiles
       if (loaders) {
-        // Each thread's 16-byte pieces of the k-step: 128 threads take
-        // consecutive pieces of the pass's units, [64 k-rows x w columns] with
-        // rows of 2w bytes.
+        // Units of [64 k-rows x w columns] with rows of 2w bytes, consecutive
+        // threads on consecutive 16-byte pieces: one of each unit per thread
+        // (w = 16), or two 32 rows apart (w = 32).
         int done_ring = ring;                 // stage whose copies are waited for next
-        const int pieces = nu * w * 8 / 128;
-        const int lw = w == 32 ? 5 : 4;
+        const int row = t / (w / 8), c = t % (w / 8), sw = (row >> (w == 32 ? 1 : 2)) & (w / 8 - 1);
+        const uint32_t dst = b_ring + static_cast<uint32_t>(row * 2 * w + ((c ^ sw) << 4));
         for (int j = 0; j < steps + kAhead && ok; ++j) {
           if (j < steps) {
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[ring], parity ^ 1u, p.err, kErrTimeoutEmpty));
             if (!ok) break;
-            const uint32_t b_s = b_ring + static_cast<uint32_t>(ring) * b_bytes;
-            const int64_t kx = static_cast<int64_t>(k_lo + j) * kBK;
-            for (int q = 0; q < pieces; ++q) {
-              const int i = q * 128 + t;
-              const int u = i >> (lw + 3), rem = i & (8 * w - 1), row = rem >> (lw - 3), c = rem & (w / 8 - 1);
-              const int sw = (row >> (lw == 5 ? 1 : 2)) & (w / 8 - 1);
-              const int2 unit = unit_list[u];
-              const bool in = kx + row < p.kc;
-              const uint16_t *src = p.R + (static_cast<int64_t>(unit.x) * p.kc + (in ? kx + row : 0)) * p.r + unit.y + c * 8;
-              cp_async16(b_s + static_cast<uint32_t>(u) * unit_bytes +
-                             static_cast<uint32_t>(row * 2 * w + ((c ^ sw) << 4)),
-                         src, in ? 16u : 0u);
+            uint32_t at = dst + static_cast<uint32_t>(ring) * b_bytes;
+            const int64_t kr = static_cast<int64_t>(k_lo + j) * kBK + row;
+            // Rows past the end are zeros.
+            const uint32_t in0 = kr < p.kc ? 16u : 0u, in1 = kr + 32 < p.kc ? 16u : 0u;
+            const int64_t off0 = (in0 ? kr : 0) * p.r + c * 8, off1 = (in1 ? kr + 32 : 0) * p.r + c * 8;
+#pragma unroll 4
+            for (int u = 0; u < nu; ++u, at += unit_bytes) {
+              const uint16_t *src = unit_src[u];
+              cp_async16(at, src + off0, in0);
+              if (w == 32) cp_async16(at + 2048u, src + off1, in1);
             }
             if (++ring == stages) {
               ring = 0;
