@@ -587,10 +587,10 @@ size_t qlora_multi_workspace_bytes(int op, int64_t m, int64_t n, int64_t k, int3
       count > QLORA_MULTI_MAX_ADAPTERS)
     return SIZE_MAX;
   const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
-  const size_t tiles = m > 0 ? round_up(tile_lists_bytes(m, count)) : 0;
+  const size_t lists = m > 0 ? round_up(tile_lists_bytes(m, count)) + round_up(group_rows_bytes(m, count)) : 0;
   switch (op) {
-    case QLORA_OP_FWD: return mr + (m > kSmallM ? tiles : 0);
-    case QLORA_OP_LORA_BWD: return 2 * mr + tiles + round_up(m > 0 ? group_rows_bytes(m, count) : 0);
+    case QLORA_OP_FWD: return mr + (m > kSmallM ? lists : 0);
+    case QLORA_OP_LORA_BWD: return 2 * mr + lists;
     default: return SIZE_MAX;
   }
 }
@@ -618,9 +618,12 @@ int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight 
   } else {
     const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
     const int64_t steps = w->k / 64;
-    const TileLists lists =
-        carve_tile_lists(static_cast<uint8_t *>(ws) + mr, m, a->count, multi_tile_rows(m, w->n, steps));
-    e = launch_multi_proj(X, m, w->k, ad, false, T, &lists, nullptr, multi_grid(m, w->n, steps, lists.rows), s);
+    uint8_t *p = static_cast<uint8_t *>(ws) + mr;
+    const TileLists lists = carve_tile_lists(p, m, a->count, multi_tile_rows(m, w->n, steps));
+    const GroupRows rows = carve_group_rows(p + round_up(tile_lists_bytes(m, a->count)), m, a->count);
+    e = launch_multi_lists(ad, m, lists, rows, T, nullptr, s);
+    if (e == cudaSuccess)
+      e = launch_multi_proj(X, m, w->k, ad, false, T, rows, multi_grid(m, w->n, steps, lists.rows), s);
     if (e == cudaSuccess) e = tc_multi(X, m, view(w), false, T, ad, lists, Y, s);
   }
   return cuda_status(e);
@@ -664,11 +667,10 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   const int64_t steps = (n + 63) / 64;
   const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, steps));
   const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), m, a->count);
-  cudaError_t e = cudaSuccess;
-  if (!T) e = launch_multi_proj(X, m, k, ad, false, Tw, nullptr, nullptr, MultiGrid{}, s);    // T = s_a X A_a^T
+  cudaError_t e = launch_multi_lists(ad, m, lists, rows, U, T ? nullptr : Tw, s);
+  if (e == cudaSuccess && !T) e = launch_multi_proj(X, m, k, ad, false, Tw, rows, MultiGrid{}, s);   // T = s_a X A_a^T
   if (e == cudaSuccess)                                                                       // U = s_a dY B_a
-    e = launch_multi_proj(dY, m, n, ad, true, U, dX ? &lists : nullptr, &rows,
-                          dX ? multi_grid(m, k, steps, lists.rows) : MultiGrid{}, s);
+    e = launch_multi_proj(dY, m, n, ad, true, U, rows, dX ? multi_grid(m, k, steps, lists.rows) : MultiGrid{}, s);
   if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);        // dX = dY W^ + U A_a
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
   if (e == cudaSuccess)

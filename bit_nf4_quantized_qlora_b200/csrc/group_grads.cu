@@ -39,6 +39,7 @@
 #include <cuda.h>
 
 #include "act8.cuh"
+#include "group_rows.cuh"
 #include "internal.h"
 #include "multi.cuh"
 #include "split_reduce.cuh"
@@ -46,9 +47,10 @@
 namespace qlora {
 namespace {
 
-constexpr int kSlot = 64;                 // rows of a step
+constexpr int kSlot = kSlotRows;          // rows of a step
 constexpr int kEpiWarps = 8;              // expand / result warps: four lane quadrants x two column halves
-constexpr int kThreads = 64 + 32 * kEpiWarps;     // and a TMA warp and an MMA warp
+constexpr int kFirstGather = 2 + kEpiWarps;
+constexpr int kThreads = 32 * (kFirstGather + 2);   // and a TMA warp, an MMA warp, two gather warps
 constexpr uint32_t kLBytes = 128u * kSlot * 2u;   // bf16 tile: two 64-column slabs
 constexpr uint32_t kRBytes = 64u * kSlot * 2u;
 constexpr uint32_t kCBytes = 128u * kSlot;        // code tile
@@ -73,77 +75,11 @@ struct __align__(64) GroupParams {
   CUtensorMap tmL, tmLg;        // L by boxes of 64 rows / by single rows
   CUtensorMap tmR, tmRg;        // R likewise
   const uint16_t *scale;        // checkpoint scales [m x P / 64]
-  const int32_t *list;          // row lists (null: one group of all rows, in order)
-  const int32_t *start, *count; // first entry (a multiple of 64) and rows of each group
+  RowSlots rows;
   uint16_t *out;                // [groups x P x r], or [groups x r x P] transposed
   unsigned *err;
   int64_t P;
-  int m, r, rtiles, groups;
-};
-
-// A CTA's part of a group: slots [b, e) of the group's [s, s + slots()).
-struct Part {
-  int group, s, rows, b, e;
-  __device__ __forceinline__ int slots() const { return (rows + kSlot - 1) / kSlot; }
-  __device__ __forceinline__ bool live() const { return b < e; }
-  __device__ __forceinline__ bool from_left() const { return b > s; }
-  __device__ __forceinline__ bool to_right() const { return e < s + slots(); }
-};
-
-// Walks the groups whose first slot or any slot lies in [lo, hi), by whole
-// warps; lane l holds group base + l.  Groups' first slots ascend strictly.
-struct GroupWalk {
-  const int32_t *start, *count;
-  int groups, lo, hi, m;
-  int a, base, s, c;
-  __device__ __forceinline__ void window(int first) {
-    base = first;
-    const int g = first + static_cast<int>(lane_id());
-    const bool in = g < groups;
-    s = !in ? 0x7FFFFFFF : (start ? __ldg(start + g) / kSlot : 0);
-    c = !in ? 0 : (start ? __ldg(count + g) : m);
-  }
-  __device__ __forceinline__ GroupWalk(const GroupParams &p, int lo_, int hi_)
-      : start(p.list ? p.start : nullptr), count(p.count), groups(p.groups), lo(lo_), hi(hi_), m(p.m) {
-    // The last group that starts at or before lo.
-    int first = 0;
-    for (int span = groups; span > 32;) {
-      const int step = (span + 31) / 32, g = first + static_cast<int>(lane_id()) * step;
-      const bool le = g < first + span && __ldg(start + g) / kSlot <= lo;
-      const int n = __popc(__ballot_sync(0xffffffffu, le));
-      first += (n - 1) * step;
-      span = groups - first < step ? groups - first : step;
-    }
-    window(first);
-    a = first + __popc(__ballot_sync(0xffffffffu, s <= lo)) - 1;
-  }
-  // The next group with slots in the share, or (with `empty`) without rows;
-  // false when there is none.
-  __device__ __forceinline__ bool next(Part *p, bool empty = false) {
-    for (;; ++a) {
-      if (a >= groups) return false;
-      if (a >= base + 32) window(a);
-      const int gs = __shfl_sync(0xffffffffu, s, a - base), gc = __shfl_sync(0xffffffffu, c, a - base);
-      if (gs >= hi) return false;
-      const int end = gs + (gc + kSlot - 1) / kSlot;
-      *p = Part{a, gs, gc, gs > lo ? gs : lo, end < hi ? end : hi};
-      if (p->live() || (empty && gc == 0 && gs >= lo)) {
-        ++a;
-        return true;
-      }
-    }
-  }
-};
-
-// The slots of a share in order.
-struct SlotWalk {
-  GroupWalk walk;
-  Part part{0, 0, 0, 0, 0};
-  __device__ __forceinline__ SlotWalk(const GroupParams &p, int lo, int hi) : walk(p, lo, hi) {}
-  __device__ __forceinline__ int next() {
-    if (part.b >= part.e && !walk.next(&part)) return -1;
-    return part.b++;
-  }
+  int r, rtiles;
 };
 
 // The warp's 32 accumulator columns of this thread's row.
@@ -206,18 +142,19 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   constexpr int kStages = stages<ACT8>();
   constexpr uint32_t kStageBytes = stage_bytes<ACT8>();
   constexpr uint32_t kIdesc = make_idesc(64, true, true);
+  constexpr int kParts = ACT8 ? 2 : 3;        // warps that fill a slot
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full[kStages], expanded[kStages], empty[kStages];
   __shared__ __align__(8) uint64_t acc_full[3], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ Part left_s, right_s;
+  __shared__ int4 gather[3][kSlot / 4];
 
   const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int p_tile = tile / p.rtiles, r_tile = tile % p.rtiles;
   // All slots, and this CTA's share of them.
-  const int slots = p.list ? __ldg(p.start + p.groups - 1) / kSlot + (__ldg(p.count + p.groups - 1) + kSlot - 1) / kSlot
-                           : (p.m + kSlot - 1) / kSlot;
+  const int slots = slot_count(p.rows);
   const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
   const auto share = [&](int i) { return static_cast<int>((static_cast<int64_t>(slots) * i) / nz); };
   const int lo = share(z), hi = share(z + 1);
@@ -228,7 +165,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kParts);
       mbar_init(&expanded[s], kEpiWarps);
       mbar_init(&empty[s], 1);
     }
@@ -248,36 +185,57 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    SlotWalk walk(p, lo, hi);
+  if (warp == 0 || warp >= kFirstGather) {
+    // ------------------------------------------------------------ producers
+    // Warp 0 announces a slot's bytes and copies boxes; gathers are shared
+    // out: L's two slabs (or its codes) and R, a warp each.  Every one of them
+    // takes part in every slot, so that none can run ahead of the others or
+    // fall behind by a whole phase of a stage.
+    const int part = warp == 0 ? 0 : warp - kFirstGather + 1;
+    SlotWalk walk(p.rows, lo, hi);
+    const auto rows_in = [&](int slot) {
+      const int left = walk.part.rows - (slot - walk.part.s) * kSlot;
+      return left < kSlot ? left : kSlot;
+    };
     // A slot's rows, four per lane on lanes 0..15; requested a slot ahead.
     const auto rows_of = [&](int slot) {
       const int r4 = slot * kSlot + 4 * lane;
-      if (!p.list || slot < 0 || lane >= 16) return make_int4(r4, r4 + 1, r4 + 2, r4 + 3);
-      return __ldg(reinterpret_cast<const int4 *>(p.list + static_cast<int64_t>(slot) * kSlot) + lane);
+      if (!p.rows.list || slot < 0 || lane >= 16) return make_int4(r4, r4 + 1, r4 + 2, r4 + 3);
+      return __ldg(reinterpret_cast<const int4 *>(p.rows.list + static_cast<int64_t>(slot) * kSlot) + lane);
     };
     int issued = 0;
-    int slot = walk.next();
+    int slot = walk.next(), valid_next = rows_in(slot);
     int4 ahead = rows_of(slot);
-    while (slot >= 0) {
+    while (slot >= 0 && part < kParts) {
       const int4 idx = ahead;
-      const int s = issued % kStages;
+      const int s = issued % kStages, valid = valid_next;
+      const uint32_t ph = (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u;
       slot = walk.next();
+      valid_next = rows_in(slot);
       ahead = rows_of(slot);
+      ++issued;
       const int first = __shfl_sync(0xffffffffu, idx.x, 0);
       const int want = first + 4 * lane;
       const bool in_order = idx.x == want && idx.y == want + 1 && idx.z == want + 2 && idx.w == want + 3;
       const bool box = __all_sync(0xffffffffu, lane >= 16 || in_order) != 0;
       const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
       const uint32_t r_s = l_s + kLBytes, c_s = r_s + kRBytes;
-      const int ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u,
-                                                               p.err, kErrTimeoutEmpty));
-      if (!ok) break;
-      if (elect_lane()) mbar_arrive_expect_tx(&full[s], (ACT8 ? kCBytes : kLBytes) + kRBytes);
-      __syncwarp();
-      if (box) {
-        if (elect_lane()) {
+      // The product takes whole 16s of rows.
+      const uint32_t chunks = box ? kSlot / 16u : static_cast<uint32_t>(valid + 15) / 16u;
+      if (!box) {
+        __syncwarp();
+        if (lane < 16) gather[part][lane] = idx;
+        __syncwarp();
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ph, p.err, kErrTimeoutEmpty))) {
+        --issued;
+        break;
+      }
+      if (elect_lane()) {
+        if (part == 0) mbar_arrive_expect_tx(&full[s], chunks * ((ACT8 ? kCBytes : kLBytes) + kRBytes) / (kSlot / 16u));
+        if (box && part > 0) {
+          // Warp 0's.
+        } else if (box) {
           if (ACT8) {
             tma_load_2d(c_s, &p.tmL, &full[s], p0, first);
           } else {
@@ -285,27 +243,25 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
             tma_load_2d(l_s + 8192u, &p.tmL, &full[s], p1, first);
           }
           tma_load_2d(r_s, &p.tmR, &full[s], r0, first);
-        }
-      } else if (lane < 16) {
-        const uint32_t row = static_cast<uint32_t>(lane) * 512u;   // four rows of 128 bytes
-        if (ACT8) {
-          tma_gather4(c_s + row, &p.tmLg, &full[s], p0, idx);
         } else {
-          tma_gather4(l_s + row, &p.tmLg, &full[s], p0, idx);
-          tma_gather4(l_s + 8192u + row, &p.tmLg, &full[s], p1, idx);
+          const bool right = part == (ACT8 ? 1 : 2);
+          const CUtensorMap *map = right ? &p.tmRg : &p.tmLg;
+          const uint32_t dst = right ? r_s : ACT8 ? c_s : l_s + static_cast<uint32_t>(part) * 8192u;
+          const int x = right ? r0 : part == 1 ? p1 : p0;
+          for (uint32_t i = 0; i < 4u * chunks; ++i)     // four rows of 128 bytes
+            tma_gather4(dst + i * 512u, map, &full[s], x, gather[part][i]);
         }
-        tma_gather4(r_s + row, &p.tmRg, &full[s], r0, idx);
+        if (part > 0) mbar_arrive(&full[s]);
       }
-      ++issued;
     }
     __syncwarp();
     // Every issued copy has landed before the CTA may exit.
-    if (lane == 0)
+    if (part == 0 && lane == 0)
       for (int li = issued - kStages < 0 ? 0 : issued - kStages; li < issued; ++li)
         mbar_wait_bounded(&full[li % kStages], static_cast<uint32_t>(li / kStages) & 1u, p.err, kErrTimeoutDrain);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    GroupWalk walk(p, lo, hi);
+    GroupWalk walk(p.rows, lo, hi);
     Part part;
     int ok = 1, turn = 0, s = 0;
     uint32_t parity = 0u;
@@ -339,7 +295,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       const uint32_t buf = left ? kLeftAcc : static_cast<uint32_t>(turn & 1);
       const uint32_t acc = tmem + buf * 64u;
       // Whole slots, then (if it is in this share) a last one with pad rows.
-      const int whole = p.list ? part.s + part.rows / kSlot : part.e;
+      const int whole = p.rows.list ? part.s + part.rows / kSlot : part.e;
       const int stop = whole < part.e ? whole : part.e;
       if (!left)
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[buf], (static_cast<uint32_t>(turn >> 1) & 1u) ^ 1u, p.err,
@@ -377,7 +333,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     const int quad = warp & 3, half = (warp - 2) >> 2;      // TMEM lanes, 32 of the 64 columns
     const uint32_t row = static_cast<uint32_t>(quad * 32 + lane);
     const int rc = r0 + 32 * half;
-    GroupWalk results(p, lo, z + 1 == nz ? 0x7FFFFFFF : hi);
+    GroupWalk results(p.rows, lo, z + 1 == nz ? 0x7FFFFFFF : hi);
     int turn = 0;
     Part part;
     bool more = results.next(&part, true);
@@ -425,14 +381,14 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       const auto row_of = [&](int slot) -> int64_t {
         if (slot < 0) return -1;
         const int64_t i = static_cast<int64_t>(slot) * kSlot + erow;
-        return p.list ? __ldg(p.list + i) : (i < p.m ? i : -1);
+        return p.rows.list ? __ldg(p.rows.list + i) : (i < p.rows.m ? i : -1);
       };
       const auto scale_of = [&](int64_t gr) -> uint32_t {
         return (gr >= 0 && cb < kb) ? static_cast<uint32_t>(__ldg(p.scale + gr * kb + cb)) : 0u;
       };
       // Scales two slots ahead, row numbers three: requested after a slot's
       // proxy fence, which would wait for them.
-      SlotWalk walk(p, lo, hi);
+      SlotWalk walk(p.rows, lo, hi);
       int slot = walk.next(), slot1 = slot < 0 ? -1 : walk.next(), slot2 = slot1 < 0 ? -1 : walk.next();
       uint32_t s0 = scale_of(row_of(slot)), s1 = scale_of(row_of(slot1));
       int64_t row2 = row_of(slot2);
@@ -569,11 +525,16 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
 }
 
 template <bool ACT8>
-cudaError_t launch(const GradsParams &p, int tiles, int split, cudaStream_t stream) {
+cudaError_t launch(const GradsParams &p, int tiles, int64_t slots, cudaStream_t stream) {
   static std::atomic<bool> configured[kMaxDevicesPerProcess] = {};
-  cudaError_t e = set_smem_once(reinterpret_cast<const void *>(group_grads_kernel<ACT8>), static_cast<int>(kSmem),
-                                configured);
+  static ClusterFit fit;
+  const void *kernel = reinterpret_cast<const void *>(group_grads_kernel<ACT8>);
+  cudaError_t e = set_smem_once(kernel, static_cast<int>(kSmem), configured);
   if (e != cudaSuccess) return e;
+  // Two slots to a CTA at least; the largest clusters that all fit at once.
+  const int most_split = static_cast<int>(slots / 2 < 1 ? 1 : slots / 2 < 8 ? slots / 2 : 8);
+  int clusters = 1;
+  const int split = fit.split(kernel, kThreads, static_cast<int>(kSmem), tiles, 2, most_split, &clusters);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(split));
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -605,18 +566,12 @@ bool group_params(GroupParams *p, const uint16_t *L, const Act8View *L8, int64_t
   }
   if (!encode_bf16_map(&p->tmR, R, m, r, 64, kSlot)) return false;
   if (!encode_bf16_map(&p->tmRg, R, m, r, 64, 1)) return false;
-  if (g) {
-    p->list = g->list;
-    p->start = g->start;
-    p->count = g->count;
-  }
+  p->rows = row_slots(g, m);
   p->out = out;
   p->err = device_error_word();
   p->P = P;
-  p->m = static_cast<int>(m);
   p->r = r;
   p->rtiles = (r + 63) / 64;
-  p->groups = g ? g->groups : 1;
   return true;
 }
 
@@ -630,17 +585,9 @@ cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint
   if (dB && !group_params(&p.db, dY, nullptr, m, n, T, r, g, dB)) return cudaErrorInvalidValue;
   p.da_tiles = static_cast<int>((k + 127) / 128) * p.da.rtiles;
   const int tiles = p.da_tiles + (dB ? static_cast<int>((n + 127) / 128) * p.db.rtiles : 0);
-  // At most m / 64 slots, and one more for every group with rows, two of
-  // them to a CTA at least; the largest clusters that all fit at once.
-  const int64_t busy = p.da.groups < m ? p.da.groups : m;
-  const int64_t slots = m / kSlot + busy;
-  static ClusterFit fit[2];
-  const void *kernel = X8 ? reinterpret_cast<const void *>(group_grads_kernel<true>)
-                          : reinterpret_cast<const void *>(group_grads_kernel<false>);
-  int clusters = 1;
-  const int split = fit[X8 ? 1 : 0].split(kernel, kThreads, kSmem, tiles, 2,
-                                          static_cast<int>(slots / 2 < 1 ? 1 : slots / 2 < 8 ? slots / 2 : 8), &clusters);
-  return X8 ? launch<true>(p, tiles, split, stream) : launch<false>(p, tiles, split, stream);
+  // At most m / 64 slots, and one more for every group with rows.
+  const int64_t slots = m / kSlot + (p.da.rows.groups < m ? p.da.rows.groups : m);
+  return X8 ? launch<true>(p, tiles, slots, stream) : launch<false>(p, tiles, slots, stream);
 }
 
 }  // namespace qlora

@@ -217,6 +217,7 @@ int choose_split(int64_t tiles, int ksteps, int per_sm = 2);
 // SMs / size).
 struct ClusterFit {
   std::atomic<int> resident[kMaxDevicesPerProcess][9];
+  // `kernel` may use smem_bytes already (set_smem_once).
   // The largest cluster size <= most_split of which `tiles` fit at once (1 if
   // none does), with per_sm CTAs to an SM (the runtime counts one);
   // *clusters is how many of that size do.
@@ -253,18 +254,29 @@ size_t tile_lists_bytes(int64_t m, int32_t count);
 // k-steps with many adapters.
 int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps);
 
+// Each adapter's rows in ascending order: list[start[a] .. + count[a]), start
+// a multiple of 64, padded to whole 64s with the adapter's last row.
+struct GroupRows {
+  int32_t *start, *count, *list;
+  int32_t groups;
+};
+GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups);
+size_t group_rows_bytes(int64_t m, int32_t groups);
+
+// Fills both kinds of lists, and with zeros the rows without an adapter of up
+// to two [m x r] results (null: none).  m > 0.
+cudaError_t launch_multi_lists(const AdapterView &s, int64_t m, const TileLists &tiles, const GroupRows &rows,
+                               uint16_t *zero0, uint16_t *zero1, cudaStream_t stream);
 // out[m x r] = bf16(s_a . L . A_a^T) (L = X [m x k]) or, through_b,
-// bf16(s_a . L . B_a) (L = dY [m x n]); zeros in rows without an adapter.
-// Fills `lists` and `rows` too unless null.  m > 0.
-struct GroupRows;
+// bf16(s_a . L . B_a) (L = dY [m x n]) in the rows that have an adapter, as a
+// programmatic dependent of the kernel before it on the stream.
 // `next` is the product launched on its heels, if any (see multi_grid).
 struct MultiGrid {
   int64_t ctas;     // one to an SM
   int64_t steps;    // 64-wide k-steps of each before it needs the projection
 };
 cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const AdapterView &s, bool through_b,
-                              uint16_t *out, const TileLists *lists, const GroupRows *rows, MultiGrid next,
-                              cudaStream_t stream);
+                              uint16_t *out, const GroupRows &rows, MultiGrid next, cudaStream_t stream);
 // tc_multi's grid on tiles of `rows` rows (multi_tile_rows).
 MultiGrid multi_grid(int64_t m, int64_t cols, int64_t ksteps, int rows);
 // The first form for m <= 16 (no lists).
@@ -278,15 +290,6 @@ cudaError_t tc_multi(const uint16_t *L, int64_t m, const WeightView &w, bool bwd
                      const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream);
 cudaError_t fused_multi_large(const uint16_t *L, int64_t m, const WeightView &w, bool bwd, const uint16_t *V,
                               const AdapterView &ad, const TileLists &lists, uint16_t *out, cudaStream_t stream);
-
-// Each adapter's rows in ascending order: list[start[a] .. + count[a]), start
-// a multiple of 64, padded to whole 64s with the adapter's last row.
-struct GroupRows {
-  int32_t *start, *count, *list;
-  int32_t groups;
-};
-GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups);
-size_t group_rows_bytes(int64_t m, int32_t groups);
 
 // An 8-bit activation checkpoint: int8 codes [m x k], bf16 scales [m x k/64].
 struct Act8View {

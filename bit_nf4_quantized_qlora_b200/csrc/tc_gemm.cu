@@ -694,7 +694,6 @@ int ClusterFit::split(const void *kernel, int threads, int smem_bytes, int64_t t
   for (int s = most_split > 8 ? 8 : most_split; s >= 1; --s) {
     int n = slot ? resident[dev][s].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
       cudaLaunchConfig_t cfg{};
       cfg.gridDim = dim3(1, 1, static_cast<unsigned>(s));
       cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
