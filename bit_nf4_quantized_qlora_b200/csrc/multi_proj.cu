@@ -412,7 +412,10 @@ cudaError_t launch_multi_proj(const uint16_t *L, int64_t m, int64_t kc, const Ad
   p.nk = static_cast<int>((kc + kBK - 1) / kBK);
   // At most m / 64 slots, and one more for every adapter with rows.
   const int64_t slots = m / kSlotRows + (s.count < m ? s.count : m);
-  const int64_t free_sms = next.ctas > 0 ? 148 - next.ctas : 0;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t free_sms = next.ctas > 0 ? sms - next.ctas : 0;
   return through_b ? launch<true>(p, slots, free_sms, next.steps, stream)
                    : launch<false>(p, slots, free_sms, next.steps, stream);
 }

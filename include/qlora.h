@@ -312,8 +312,9 @@ int qlora_linear_bwd_dx_dropout(const uint16_t *dY, int64_t m, const qlora_nf4_w
  *     c     = max |x|,   scale = bf16_rne(c / 127)
  *     codes = clamp(rint_even(x / scale), -127, 127)     (0 when scale == 0)
  *     X^    = bf16_rne(codes . scale)
- * so |X^ - x| <= scale / 2 plus one bf16 rounding.  x is finite and below
- * 2^127 in magnitude.
+ * so |X^ - x| <= scale / 2 plus one bf16 rounding, for x finite and below
+ * 2^127 in magnitude.  A block with an infinity or a NaN restores without a
+ * finite value.
  *   codes  int8 [m x k] row-major;  scale  bf16 [m x k/64];  m >= 0, k % 64 == 0
  * One checkpoint serves every layer with the same input (q, k and v).        */
 typedef struct {
