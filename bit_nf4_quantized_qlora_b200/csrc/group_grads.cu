@@ -156,7 +156,10 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   // All slots, and this CTA's share of them.
   const int slots = slot_count(p.rows);
   const int z = static_cast<int>(blockIdx.z), nz = static_cast<int>(gridDim.z);
-  const auto share = [&](int i) { return static_cast<int>((static_cast<int64_t>(slots) * i) / nz); };
+  // No CTA between two with slots is without: a group that crosses borders is
+  // finished by consecutive CTAs, each with a partial.
+  const int busy = slots < nz ? (slots > 0 ? slots : 1) : nz;
+  const auto share = [&](int i) { return i < busy ? static_cast<int>((static_cast<int64_t>(slots) * i) / busy) : slots; };
   const int lo = share(z), hi = share(z + 1);
   const int p0 = p_tile * 128, r0 = r_tile * 64;
   // Second 64-column slab; past P it repeats the first (its output rows are

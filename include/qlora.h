@@ -354,8 +354,10 @@ int qlora_linear_bwd_act8(const uint16_t *dY, const qlora_act8 *x8, const uint16
  *
  * Rows of one adapter that lie together cost least (their products share
  * tiles); any order is correct, and no row's result depends on another
- * adapter's rows or values.  Results do not depend on timing (no
- * floating-point atomics).                                                   */
+ * adapter's rows or values.  Results do not depend on timing, with one
+ * exception: for m <= 4 the forward's streaming kernel (qlora_linear_fwd's too)
+ * adds its warps' fp32 sums in the order they come, so that a last bit of Y may
+ * differ between runs.                                                       */
 #define QLORA_MULTI_MAX_ADAPTERS 65535
 #define QLORA_MULTI_MAX_ROWS (1 << 22)
 typedef struct {

@@ -14,6 +14,7 @@ import multi_refs as M
 import oracle_refs as R
 from bit_nf4_quantized_qlora_b200 import binding as B
 from bit_nf4_quantized_qlora_b200 import workloads as WL
+from oracle import act8
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -181,6 +182,26 @@ def test_batches_of_many_tiles(order):
     got = B.qlora_linear_bwd_multi(c.dY.to(DEV), c.X.to(DEV), c.weight(DEV), A, Bm, s, ids, T=T.to(DEV))
     c.check_bwd(got, c.Xf, R.bf16_to_f64(T))
     assert B.qlora_poll_device_error() == 0
+
+
+@pytest.mark.parametrize("r", [16, 64, 80])
+@pytest.mark.parametrize("few", [1, 64, 65, 177, 300])
+@pytest.mark.parametrize("count", [1, 3])
+def test_few_rows_with_an_adapter_among_many_without(few, count, r):
+    """Fewer 64-row slots than the batch has room for: gradients of a group
+    that crosses CTAs, some of which have no slot."""
+    m, n, k = 1200, 264, 192
+    c = M.case(m, n, k, r, count, "none", 11700 + few + r)
+    g = np.random.default_rng(few)
+    ids = np.full(m, -1, dtype=np.int32)
+    ids[g.choice(m, few, replace=False)] = count - 1
+    c = M.Case(c.W, c.X, c.dY, c.A, c.B, c.scale, torch.from_numpy(ids))
+    A, Bm, s, idd = c.on(DEV)
+    c.check_fwd(B.qlora_linear_fwd_multi(c.X.to(DEV), c.weight(DEV), A, Bm, s, idd))
+    T = _T(c)
+    for X, Xf in ((c.X.to(DEV), c.Xf), (B.qlora_act_quantize(c.X.to(DEV)), act8.dequant_values(*act8.quantize(c.Xf)))):
+        got = B.qlora_linear_bwd_multi(c.dY.to(DEV), X, c.weight(DEV), A, Bm, s, idd, T=T.to(DEV))
+        c.check_bwd(got, Xf, R.bf16_to_f64(T))
 
 
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
