@@ -17,7 +17,7 @@
 // 2000 x 4096 through 32 rank-16 adapters in any order and 181 us for
 // 1111 x 11008 through 64 rank-64 ones.)  K is split over a cluster of up to 8
 // CTAs whose fp32 partials are added in rank order through distributed shared
-// memory; two CTAs share an SM for r <= 128.  A stage holds 128 columns: a warp
+// memory; two CTAs share an SM for r <= 64.  A stage holds 128 columns: a warp
 // takes about 230 cycles for the waits and the loop around a stage and 50 for
 // every copy it issues, so with stages of 64 columns and one issuing warp the
 // slots with gathered rows took 1100 cycles each; the idle epilogue warps issue
@@ -44,9 +44,12 @@ constexpr int kThreads = 192;
 constexpr uint32_t kABytes = static_cast<uint32_t>(kSlotRows) * kBK * 2u;   // 8 KB, half a stage's
 constexpr uint32_t kColBytes = kBK * 2u;          // shared memory of one rank column of a copy
 constexpr uint32_t kTmemCols = 256;               // r <= 256
-// One CTA to an SM, or two with half the ring each for ranks up to 128.
+// One CTA to an SM, or two with half the ring each for ranks up to 64, where a
+// half still holds three stages (backward of 2000 x 4096, r = 16, 32 adapters:
+// 100 us with two and 103 with one; of 4096 x 11008, r = 128, 8 adapters: 448
+// with two of two stages and 426 with one of four).
 constexpr uint32_t kRing = 200u * 1024u;
-constexpr int kSharedRank = 128;
+constexpr int kSharedRank = 64;
 constexpr int stages_of(int r, int per_sm) {
   const int s = static_cast<int>(kRing / static_cast<uint32_t>(per_sm) / (2u * (kABytes + static_cast<uint32_t>(r) * kColBytes)));
   return s < kMaxStages ? s : kMaxStages;
@@ -354,9 +357,13 @@ cudaError_t launch(ProjParams &p, int64_t slots, int64_t free_sms, int64_t main_
   cudaError_t e = set_smem_once(kernel, static_cast<int>(kRing) + 1024, configured);
   if (e != cudaSuccess) return e;
   // The projection keeps to the SMs that the product launched on its heels
-  // leaves free, if it is done there before that product needs it (a slot's
-  // k-step takes 0.3 to 0.5 us, the product's 0.55 to 0.85 us); one CTA to an
-  // SM then, since CTAs that could share one are spread over them all.
+  // leaves free, if it is done there before that product needs it: 64 columns
+  // of a slot take about 0.33 us, a k-step of the product 0.55 to 0.85 us.
+  // Forward of 1111 x 11008 -> 4096, r = 64: 123 us beside the product and 139
+  // in front of it with 6 adapters, 193 and 191 with 64 (where the estimate is
+  // the product's whole main loop); 128 x 8192 -> 28672, r = 16, 64 adapters: 123
+  // and 137.  One CTA to an SM then, since CTAs that could share one are spread
+  // over them all.
   // K is split over the largest clusters of which one per slot fits at once.
   const bool beside = free_sms >= 16 && slots * p.nk <= 2 * free_sms * main_steps;
   const int per_sm = beside || p.r > kSharedRank ? 1 : 2;
