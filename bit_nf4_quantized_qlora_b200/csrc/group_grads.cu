@@ -35,7 +35,9 @@
 // Checkpoint form: L's tile arrives as 64 x 128 codes (half the bytes); the
 // eight epilogue warps expand it to the bf16 tile the product reads, half a
 // block of 64 elements (one scale) per thread: two integer and half a packed
-// floating-point instruction per element.
+// floating-point instruction per element.  dA of 11008 x 64 from 4096 rows: 32 us,
+// 1.5 TB/s of codes; a slot is a chain of about 1300 cycles in the expand warps
+// (two groups of four warps in turn, with two bf16 tiles, took the same time).
 #include <cuda.h>
 
 #include "act8.cuh"
@@ -68,7 +70,7 @@ constexpr uint32_t stage_bytes() { return kLBytes + kRBytes + (ACT8 ? kCBytes : 
 constexpr uint32_t kRing = stage_bytes<false>() * stages<false>();
 constexpr uint32_t kSmem = kRing + 1024u;
 static_assert(kRing == stage_bytes<true>() * stages<true>(), "the two forms share a kernel");
-static_assert(2u * (kSmem + 2048u) <= 227u * 1024u, "two CTAs per SM");
+static_assert(2u * (kSmem + 4096u) <= 227u * 1024u, "two CTAs per SM");
 static_assert(kRing >= 2u * kPartBytes, "room for two fp32 partial tiles");
 
 struct __align__(64) GroupParams {
@@ -142,13 +144,14 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   constexpr int kStages = stages<ACT8>();
   constexpr uint32_t kStageBytes = stage_bytes<ACT8>();
   constexpr uint32_t kIdesc = make_idesc(64, true, true);
-  constexpr int kParts = ACT8 ? 2 : 3;        // warps that fill a slot
+  constexpr int kParts = 3;                   // warps that fill a slot
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full[kStages], expanded[kStages], empty[kStages];
   __shared__ __align__(8) uint64_t acc_full[3], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ Part left_s, right_s;
   __shared__ int4 gather[3][kSlot / 4];
+  __shared__ uint2 scale_s[ACT8 ? kStages : 1][kSlot / 2];    // per row, its scales of the tile's two blocks
 
   const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -188,7 +191,48 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 0 || warp >= kFirstGather) {
+  if (ACT8 && warp == kFirstGather + 1) {
+    // ------------------------------------------------------------ scales
+    // Two rows a lane; requested a slot ahead, their row numbers two.  (In the
+    // expand warps these loads were what a slot's proxy fence waited for.)
+    SlotWalk walk(p.rows, lo, hi);
+    const int64_t kb = p.P / 64, cb = static_cast<int64_t>(p_tile) * 2;
+    const auto rows_of = [&](int slot) {
+      const int64_t i = static_cast<int64_t>(slot) * kSlot + 2 * lane;
+      if (slot < 0) return make_int2(-1, -1);
+      if (p.rows.list) return __ldg(reinterpret_cast<const int2 *>(p.rows.list + i));
+      return make_int2(i < p.rows.m ? static_cast<int>(i) : -1, i + 1 < p.rows.m ? static_cast<int>(i + 1) : -1);
+    };
+    // Packed only when they are stored: arithmetic here would wait for the loads.
+    const auto scales_of = [&](const int2 &row) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      const uint16_t *x = p.scale + static_cast<int64_t>(row.x) * kb + cb, *y = p.scale + static_cast<int64_t>(row.y) * kb + cb;
+      if (row.x >= 0) v.x = __ldg(x);
+      if (row.x >= 0 && cb + 1 < kb) v.y = __ldg(x + 1);
+      if (row.y >= 0) v.z = __ldg(y);
+      if (row.y >= 0 && cb + 1 < kb) v.w = __ldg(y + 1);
+      return v;
+    };
+    int slot = walk.next(), slot1 = slot < 0 ? -1 : walk.next(), slot2 = slot1 < 0 ? -1 : walk.next();
+    const int2 row = rows_of(slot), row1 = rows_of(slot1);
+    int2 row2 = rows_of(slot2);
+    uint4 v = scales_of(row), v1 = scales_of(row1);
+    for (int li = 0; slot >= 0; ++li) {
+      const int s = li % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], (static_cast<uint32_t>(li / kStages) & 1u) ^ 1u, p.err,
+                                                     kErrTimeoutEmpty)))
+        break;
+      scale_s[s][lane] = make_uint2(v.x | v.y << 16, v.z | v.w << 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+      v = v1;
+      v1 = scales_of(row2);
+      slot = slot1;
+      slot1 = slot2;
+      slot2 = slot2 < 0 ? -1 : walk.next();
+      row2 = rows_of(slot2);
+    }
+  } else if (warp == 0 || warp >= kFirstGather) {
     // ------------------------------------------------------------ producers
     // Warp 0 announces a slot's bytes and copies boxes; gathers are shared
     // out: L's two slabs (or its codes) and R, a warp each.  Every one of them
@@ -209,7 +253,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     int issued = 0;
     int slot = walk.next(), valid_next = rows_in(slot);
     int4 ahead = rows_of(slot);
-    while (slot >= 0 && part < kParts) {
+    while (slot >= 0) {
       const int4 idx = ahead;
       const int s = issued % kStages, valid = valid_next;
       const uint32_t ph = (static_cast<uint32_t>(issued / kStages) & 1u) ^ 1u;
@@ -379,28 +423,15 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       // ---------------------------------------------------------- expand
       // Thread t: row t / 4 of the slot, 32-column quarter t % 4.
       const int erow = t >> 2, quarter = t & 3, slab = quarter >> 1;
-      const int64_t kb = p.P / 64, cb = static_cast<int64_t>(p_tile) * 2 + slab;
       const uint32_t sw = static_cast<uint32_t>(erow & 7);
-      const auto row_of = [&](int slot) -> int64_t {
-        if (slot < 0) return -1;
-        const int64_t i = static_cast<int64_t>(slot) * kSlot + erow;
-        return p.rows.list ? __ldg(p.rows.list + i) : (i < p.rows.m ? i : -1);
-      };
-      const auto scale_of = [&](int64_t gr) -> uint32_t {
-        return (gr >= 0 && cb < kb) ? static_cast<uint32_t>(__ldg(p.scale + gr * kb + cb)) : 0u;
-      };
-      // Scales two slots ahead, row numbers three: requested after a slot's
-      // proxy fence, which would wait for them.
       SlotWalk walk(p.rows, lo, hi);
-      int slot = walk.next(), slot1 = slot < 0 ? -1 : walk.next(), slot2 = slot1 < 0 ? -1 : walk.next();
-      uint32_t s0 = scale_of(row_of(slot)), s1 = scale_of(row_of(slot1));
-      int64_t row2 = row_of(slot2);
-      for (int li = 0; slot >= 0; ++li) {
+      for (int li = 0; walk.next() >= 0; ++li) {
         const int s = li % kStages;
         const uint32_t ph = static_cast<uint32_t>(li / kStages) & 1u;
-        const uint32_t s2 = s0 * 0x10001u;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, p.err, kErrTimeoutFullA));
         if (!ok) break;
+        const uint2 sc = scale_s[s][erow >> 1];
+        const uint32_t s2 = (((erow & 1 ? sc.y : sc.x) >> (16 * slab)) & 0xFFFFu) * 0x10001u;
         const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
         const uint32_t code_row = l_s + kLBytes + kRBytes + static_cast<uint32_t>(erow) * 128u;
         const uint32_t out_row = l_s + static_cast<uint32_t>(slab) * 8192u + static_cast<uint32_t>(erow) * 128u;
@@ -421,12 +452,6 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&expanded[s]);
-        s0 = s1;
-        s1 = scale_of(row2);
-        slot = slot1;
-        slot1 = slot2;
-        slot2 = slot2 < 0 ? -1 : walk.next();
-        row2 = row_of(slot2);
         // Results two slots late: their products have had time to finish.
         flush(li - 1);
         if (!ok) break;
