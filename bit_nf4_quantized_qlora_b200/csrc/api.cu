@@ -185,13 +185,14 @@ cudaError_t launch_small_m(const uint16_t *X, int64_t m, const qlora_nf4_weight 
                            int32_t adapters) {
   // One adapter for all keeps the plain levels, whose results callers have;
   // many adapters take the ones that lose less to bf16.
-  const Nf4Tables &tab = ids ? stream_tables(w->codebook).tab : codebook_tables(w->codebook);
-  const float unscale = ids ? stream_tables(w->codebook).unscale : 1.0f;
+  const StreamTables *st = ids ? &stream_tables(w->codebook) : nullptr;
+  const Nf4Tables &plain = codebook_tables(w->codebook);
   return gemv_stream_supported(m, w->n, w->k)
              ? launch_gemv_stream(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T, B, r, Y,
-                                  tab, s, pdl, ids, adapters, unscale)
-             : launch_gemv_fwd(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T, B, r, Y, tab,
-                               s, pdl, ids, adapters, unscale);
+                                  st ? st->stream.tab : plain, s, pdl, ids, adapters, st ? st->stream.unscale : 1.0f,
+                                  st ? st->stream.offset : 0.0f)
+             : launch_gemv_fwd(X, m, w->codes, w->absmax_q, w->group_scale, view(w).mu, w->n, w->k, T, B, r, Y,
+                               st ? st->ring.tab : plain, s, pdl, ids, adapters, st ? st->ring.unscale : 1.0f);
 }
 
 }  // namespace

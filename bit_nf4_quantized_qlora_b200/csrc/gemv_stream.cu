@@ -86,6 +86,7 @@ struct __align__(64) StreamParams {
   int64_t n, k;
   int adapters;
   float unscale;                 // takes the levels' common factor out of the block constants
+  uint32_t minus_offset;         // minus the levels' offset, a bf16 pair (OFFSET kernels)
   int m, r;
   int ntiles;                    // ceil(n / tile rows)
   int chunks;                    // ceil((k / 64) / 4)
@@ -150,14 +151,14 @@ __device__ __forceinline__ void red_pair(uint32_t pred, uint32_t addr, float a, 
 // Two k-steps from one 32-bit word of each of the rows g and g+8 (8 weights
 // each): byte 0 -> a0/a1, byte 1 -> a2/a3, then bytes 2 and 3.  xv holds the
 // matching 8 activations of this lane's column.  FIRST starts the chain from
-// a zero accumulator.
-template <bool FIRST>
+// a zero accumulator, or (OFFSET) from what d holds.
+template <bool FIRST, bool OFFSET>
 __device__ __forceinline__ void word_mma(float (&d)[4], uint32_t w_g, uint32_t w_g8, const uint8_t *lut, uint32_t lane4,
                                          const uint4 &xv) {
   const auto L = [&](uint32_t off) { return *reinterpret_cast<const uint32_t *>(lut + off); };
   const uint32_t a0 = L(pair_lut_off<0>(w_g, lane4)), a1 = L(pair_lut_off<0>(w_g8, lane4));
   const uint32_t a2 = L(pair_lut_off<1>(w_g, lane4)), a3 = L(pair_lut_off<1>(w_g8, lane4));
-  if (FIRST)
+  if (FIRST && !OFFSET)
     mma_bf16_16816_zero(d, a0, a1, a2, a3, xv.x, xv.y);
   else
     mma_bf16_16816(d, a0, a1, a2, a3, xv.x, xv.y);
@@ -171,7 +172,8 @@ __device__ __forceinline__ bool slot_pass(const F &f, uint32_t ph, std::integer_
 }
 
 // FP8: the absmax codes are E4M3 offsets from the tensor mean (p.mu).
-template <int MODE, bool FP8>
+// OFFSET: the levels have one (StreamTables).
+template <int MODE, bool FP8, bool OFFSET>
 __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_constant__ StreamParams p) {
   extern __shared__ __align__(1024) uint8_t dsmem[];
   const uint8_t *lut = dsmem;
@@ -241,6 +243,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
                                                       (v ? kb0 * 64 + 64 * (2 * i + (q >> 1)) + 32 * (q & 1) : 0));
 #pragma unroll
     for (int j = 0; j < 4; ++j) xf[i][j] = v ? __ldg(xp + j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  // Minus the offset times the activations of each column's block, where the
+  // block products start (every row's is the same).
+  float start[2][2];
+  if (OFFSET) {
+    const uint32_t mo = p.minus_offset;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma_bf16_16816(d, mo, mo, mo, mo, xf[i][j].x, xf[i][j].y);
+        mma_bf16_16816(d, mo, mo, mo, mo, xf[i][j].z, xf[i][j].w);
+      }
+      start[i][0] = d[0];
+      start[i][1] = d[1];
+    }
   }
 
   // The group constant t (fp32(S / 255) for linear codes) of every group
@@ -345,10 +365,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
 #pragma unroll
         for (int st = 0; st < kSub; ++st) {
           const uint4 cg = c[st][i], cg8 = c[st][2 + i];
-          word_mma<true>(d[st], cg.x, cg8.x, lut, lane4, xf[i][0]);
-          word_mma<false>(d[st], cg.y, cg8.y, lut, lane4, xf[i][1]);
-          word_mma<false>(d[st], cg.z, cg8.z, lut, lane4, xf[i][2]);
-          word_mma<false>(d[st], cg.w, cg8.w, lut, lane4, xf[i][3]);
+          if (OFFSET) {
+            d[st][0] = d[st][2] = start[i][0];
+            d[st][1] = d[st][3] = start[i][1];
+          }
+          word_mma<true, OFFSET>(d[st], cg.x, cg8.x, lut, lane4, xf[i][0]);
+          word_mma<false, OFFSET>(d[st], cg.y, cg8.y, lut, lane4, xf[i][1]);
+          word_mma<false, OFFSET>(d[st], cg.z, cg8.z, lut, lane4, xf[i][2]);
+          word_mma<false, OFFSET>(d[st], cg.w, cg8.w, lut, lane4, xf[i][3]);
         }
         // d[st][0], d[st][1]: row pair 2st (row pr + 16 st), token q, blocks
         // 2i and 2i+1; d[st][2], d[st][3]: row pair 2st + 1 (8 rows below).
@@ -461,17 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
   cluster_sync_all();
 }
 
-template <int MODE, bool FP8>
+template <int MODE, bool FP8, bool OFFSET>
 cudaError_t configure(int dev) {
   static std::atomic<bool> done[kMaxDevicesPerProcess] = {};
   if (dev < 0 || dev >= kMaxDevicesPerProcess) return cudaErrorInvalidDevice;
-  return set_smem_once(reinterpret_cast<const void *>(gemv_stream_kernel<MODE, FP8>), static_cast<int>(kSmemBytes),
+  return set_smem_once(reinterpret_cast<const void *>(gemv_stream_kernel<MODE, FP8, OFFSET>), static_cast<int>(kSmemBytes),
                        &done[dev]);
 }
 
-template <int MODE, bool FP8>
+template <int MODE, bool FP8, bool OFFSET>
 cudaError_t launch_mode(const StreamParams &p, int dev, int sms, int cs, cudaStream_t stream, bool pdl) {
-  cudaError_t e = configure<MODE, FP8>(dev);
+  cudaError_t e = configure<MODE, FP8, OFFSET>(dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
@@ -495,7 +519,7 @@ cudaError_t launch_mode(const StreamParams &p, int dev, int sms, int cs, cudaStr
   int res = resident[dev][FP8 ? 1 : 0][cs].load(std::memory_order_relaxed);
   if (res == 0) {
     int v = 0;
-    e = cudaOccupancyMaxActiveClusters(&v, gemv_stream_kernel<MODE, FP8>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&v, gemv_stream_kernel<MODE, FP8, OFFSET>, &cfg);
     if (e != cudaSuccess) return e;
     res = v > 0 ? v : (sms / cs > 0 ? sms / cs : 1);
     resident[dev][FP8 ? 1 : 0][cs].store(res, std::memory_order_relaxed);
@@ -505,7 +529,7 @@ cudaError_t launch_mode(const StreamParams &p, int dev, int sms, int cs, cudaStr
   if (ncl < min_ncl) ncl = min_ncl;
   cfg.gridDim = dim3(static_cast<unsigned>(cs), static_cast<unsigned>(ncl), 1);
   cfg.numAttrs = (p.r > 0 && pdl) ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemv_stream_kernel<MODE, FP8>, p);
+  return cudaLaunchKernelEx(&cfg, gemv_stream_kernel<MODE, FP8, OFFSET>, p);
 }
 
 }  // namespace
@@ -519,7 +543,7 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
                                const float *group_scale, const float *mu, int64_t n, int64_t k, const uint16_t *T,
                                const uint16_t *B, int32_t r, uint16_t *Y, const Nf4Tables &tab,
                                cudaStream_t stream, bool pdl, const int32_t *ids, int32_t adapters,
-                               float unscale) {
+                               float unscale, float offset) {
   if (m <= 0) return cudaSuccess;
   if (!gemv_stream_supported(m, n, k)) return cudaErrorInvalidValue;
   const int64_t kblocks = k / 64;
@@ -536,6 +560,7 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
   p.ids = ids;
   p.adapters = adapters;
   p.unscale = unscale;
+  p.minus_offset = bf16_pair(-offset);
   p.Y = Y;
   p.err = device_error_word();
   p.n = n;
@@ -552,10 +577,15 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const bool fp8 = mu != nullptr;
-  const cudaError_t e =
-      mode == 2   ? (fp8 ? launch_mode<2, true>(p, dev, sms, cs, stream, pdl) : launch_mode<2, false>(p, dev, sms, cs, stream, pdl))
-      : mode == 1 ? (fp8 ? launch_mode<1, true>(p, dev, sms, cs, stream, pdl) : launch_mode<1, false>(p, dev, sms, cs, stream, pdl))
-                  : (fp8 ? launch_mode<0, true>(p, dev, sms, cs, stream, pdl) : launch_mode<0, false>(p, dev, sms, cs, stream, pdl));
+  const auto launch = [&](auto mode_const) {
+    constexpr int M = decltype(mode_const)::value;
+    if (offset != 0.f)
+      return fp8 ? launch_mode<M, true, true>(p, dev, sms, cs, stream, pdl) : launch_mode<M, false, true>(p, dev, sms, cs, stream, pdl);
+    return fp8 ? launch_mode<M, true, false>(p, dev, sms, cs, stream, pdl) : launch_mode<M, false, false>(p, dev, sms, cs, stream, pdl);
+  };
+  const cudaError_t e = mode == 2   ? launch(std::integral_constant<int, 2>{})
+                        : mode == 1 ? launch(std::integral_constant<int, 1>{})
+                                    : launch(std::integral_constant<int, 0>{});
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -21,14 +22,28 @@ const Nf4Tables &codebook_tables(int codebook);
 const QuantBuckets &codebook_buckets(int codebook);
 const Nf4Tables &nf4_tables();
 
-// A codebook's levels times a factor g that brings them close to bf16 numbers,
-// and 1 / g for the block constants.  The weight-streaming kernels multiply
-// bf16 levels and scale afterwards: with these tables the levels' rounding
-// costs 0.08 % (rms, NF4) instead of 0.14 %, and nothing for FP4 and INT4.
-struct StreamTables {
+// A codebook's levels as g L + h, close to bf16 numbers, with 1 / g for the
+// block constants and h (a bf16 number).  The weight-streaming kernels multiply
+// bf16 levels and scale afterwards; h times the sum of a block's activations is
+// taken off first.
+struct LevelForm {
   Nf4Tables tab;
-  float unscale;
+  float unscale, offset;
 };
+// Of both weight-streaming kernels.  With these forms the levels' rounding costs
+// 0.06 % (gemv_stream.cu) and 0.08 % (gemv.cu; rms, NF4) instead of 0.14 %, and
+// nothing for FP4 and INT4.  gemv.cu takes no offset: its activations change
+// with every stage, and their sums cost it 15 % (16 x 4096 -> 11008: 31 us
+// against 26.7, with X as either operand), while gemv_stream.cu forms them once.
+struct StreamTables {
+  LevelForm stream, ring;
+};
+// A bf16 number twice in a word.
+inline uint32_t bf16_pair(float x) {
+  uint32_t u;
+  std::memcpy(&u, &x, 4);
+  return (u >> 16) | (u & 0xFFFF0000u);
+}
 const StreamTables &stream_tables(int codebook);
 
 // Device error word (bounded waits that gave up); one per device.
@@ -137,7 +152,7 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
                                const uint8_t *absmax_q, const float *group_scale, const float *mu,
                                int64_t n, int64_t k, const uint16_t *T, const uint16_t *B, int32_t r, uint16_t *Y,
                                const Nf4Tables &tab, cudaStream_t stream, bool pdl, const int32_t *ids = nullptr,
-                            int32_t adapters = 0, float unscale = 1.0f);
+                            int32_t adapters = 0, float unscale = 1.0f, float offset = 0.0f);
 
 // tcgen05 paths -------------------------------------------------------------
 

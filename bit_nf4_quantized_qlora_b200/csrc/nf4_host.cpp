@@ -145,44 +145,28 @@ const QuantBuckets &codebook_buckets(int codebook) {
 
 namespace {
 
-float bf16_rne(float x) {
-  uint32_t u;
-  std::memcpy(&u, &x, 4);
-  u = (u + 0x7FFFu + ((u >> 16) & 1u)) & 0xFFFF0000u;
-  std::memcpy(&x, &u, 4);
-  return x;
-}
-
-// The factor g in {1 + i / 4096} whose multiples g . L lie closest to bf16
-// numbers (sum over the levels of (bf16(g L) / g - L)^2; the first minimum).
-StreamTables build_stream(const Nf4Tables &t) {
-  double best = std::numeric_limits<double>::infinity();
-  float g = 1.0f;
-  for (int i = 0; i < 4096; ++i) {
-    const float c = 1.0f + static_cast<float>(i) / 4096.0f;
-    double sum = 0.0;
-    for (int j = 0; j < 16; ++j) {
-      const double e = static_cast<double>(bf16_rne(t.level[j] * c)) / c - t.level[j];
-      sum += e * e;
-    }
-    if (sum < best) {
-      best = sum;
-      g = c;
-    }
-  }
-  StreamTables s{};
+LevelForm level_form(const Nf4Tables &t, float g, float h) {
+  LevelForm s{};
   s.tab = t;
-  for (int j = 0; j < 16; ++j) s.tab.level[j] = t.level[j] * g;
+  for (int j = 0; j < 16; ++j) s.tab.level[j] = std::fmaf(t.level[j], g, h);
   s.unscale = 1.0f / g;
+  s.offset = h;
   return s;
 }
 
 }  // namespace
 
 const StreamTables &stream_tables(int codebook) {
-  static const StreamTables s[kCodebookCount] = {build_stream(codebook_tables(kCodebookNF4)),
-                                                 build_stream(codebook_tables(kCodebookFP4)),
-                                                 build_stream(codebook_tables(kCodebookINT4))};
+  // FP4's and INT4's levels are bf16 numbers after a factor of 1.5 and 1.75.  No
+  // factor does that for NF4.  Of g = 1 + i / 2048 and h = -j / 2048, j < 256, the
+  // first pair has the smallest sum over the levels of
+  // (bf16(g L + h) - (g L + h))^2 / g^2; of g = 1 + i / 4096 alone the second, each
+  // level counted as often as normally distributed weights take it.
+  static const auto both = [](int c, float g) { return StreamTables{level_form(codebook_tables(c), g, 0.f), level_form(codebook_tables(c), g, 0.f)}; };
+  static const StreamTables s[kCodebookCount] = {
+      StreamTables{level_form(codebook_tables(kCodebookNF4), 1.0f + 1695.0f / 2048.0f, -97.0f / 2048.0f),
+                   level_form(codebook_tables(kCodebookNF4), 1.0f + 1789.0f / 4096.0f, 0.0f)},
+      both(kCodebookFP4, 1.5f), both(kCodebookINT4, 1.75f)};
   return s[(codebook >= 0 && codebook < kCodebookCount) ? codebook : kCodebookNF4];
 }
 

@@ -60,13 +60,14 @@ class Case:
         return quant.dequant_bf16_values(self.packed, self.q, self.S).reshape(self.W.shape)
 
     def W_stream(self):
-        """The weight-streaming kernels' weight: bf16(g L) scaled by c' / g
-        after the product, g in {1 + i/4096} the factor that brings the levels
-        closest to bf16 numbers."""
+        """The weight-streaming kernels' weight: bf16(g L + h) less h, scaled
+        by c' / g after the product.  Up to four rows, the pair of g = 1 + i / 2048
+        and h = -j / 2048, j < 256, that brings the levels closest to bf16 numbers;
+        above, a factor g alone."""
         L = nf4.levels_f32()
-        g = (1 + np.arange(4096) / 4096).astype(np.float32)[:, None]
-        rounded = quant.bf16_bits_to_f32(quant.bf16_rne_bits((L * g).reshape(-1))).reshape(4096, 16).astype(np.float64) / g
-        lv = rounded[np.argmin(((rounded - L) ** 2).sum(1))]
+        g, h = (1 + 1695 / 2048, -97 / 2048) if self.X.shape[0] <= 4 else (1 + 1789 / 4096, 0.0)
+        scaled = (L.astype(np.float64) * g + h).astype(np.float32)
+        lv = (quant.bf16_bits_to_f32(quant.bf16_rne_bits(scaled)).astype(np.float64) - h) / g
         c = np.repeat(quant.absmax_dequant(self.q, self.S).astype(np.float64), 64)
         return (lv[quant.unpack_codes(self.packed)] * c).reshape(self.W.shape)
 
