@@ -508,8 +508,12 @@ def _need(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, devic
 def _need_act8(act: Act8, m: int, k: int, device) -> None:
     if act.m != m or act.k != k:
         raise ValueError(f"the checkpoint holds [{act.m} x {act.k}], not [{m} x {k}]")
-    _need(act.codes, "codes", torch.int8, (m, k), device)
-    _need(act.scale, "scale", torch.bfloat16, (m, k // BLOCK), device)
+    codes, scale = act.codes, act.scale
+    if not (codes.dtype is torch.int8 and scale.dtype is torch.bfloat16 and codes.shape == (m, k)
+            and scale.shape == (m, k // BLOCK) and codes.device == device and scale.device == device
+            and codes.is_contiguous() and scale.is_contiguous()):
+        _need(codes, "codes", torch.int8, (m, k), device)
+        _need(scale, "scale", torch.bfloat16, (m, k // BLOCK), device)
 
 
 def _need_weight(w: NF4Weight, device) -> None:
@@ -542,13 +546,14 @@ def qlora_act_quantize(X: torch.Tensor, out: Optional[Act8] = None, stream=None)
     scale = bf16(max|x| / 127), codes = rint(x / scale)."""
     if X.dim() != 2 or X.shape[1] % BLOCK:
         raise ValueError("X must be a 2-D tensor with a row length that is a multiple of 64")
-    m, k = X.shape
-    _need(X, "X", torch.bfloat16, (m, k), X.device)
+    (m, k), dev = X.shape, X.device
+    if X.dtype is not torch.bfloat16 or not X.is_contiguous():
+        _need(X, "X", torch.bfloat16, (m, k), dev)
     if out is None:
-        out = Act8.empty(m, k, X.device)
-    _need_act8(out, m, k, X.device)
+        out = Act8.empty(m, k, dev)
+    _need_act8(out, m, k, dev)
     _check("qlora_act_quantize", lib().qlora_act_quantize(X.data_ptr(), m, k, out.codes.data_ptr(),
-                                                          out.scale.data_ptr(), _stream_on(X.device, stream)))
+                                                          out.scale.data_ptr(), _stream_on(dev, stream)))
     return out
 
 
@@ -595,12 +600,20 @@ def qlora_multi_workspace_bytes(op: int, m: int, n: int, k: int, r: int, count: 
 def _adapter_set(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor, m: int, w: NF4Weight, dev):
     if A.dim() != 3:
         raise ValueError("A must be a 3-D tensor [count x r x k]")
-    count, r = A.shape[0], A.shape[1]
-    _need(A, "A", torch.bfloat16, (count, r, w.k), dev)
-    _need(B, "B", torch.bfloat16, (count, w.n, r), dev)
-    _need(scale, "scale", torch.float32, (count,), dev)
-    _need(ids, "ids", torch.int32, (m,), dev)
-    _need_weight(w, dev)
+    count, r, k = A.shape
+    bf = torch.bfloat16
+    # One condition for the call that is right; the checks that name what is
+    # wrong cost a call each.
+    if not (A.dtype is bf and B.dtype is bf and scale.dtype is torch.float32 and ids.dtype is torch.int32
+            and k == w.k and B.shape == (count, w.n, r) and scale.shape == (count,) and ids.shape == (m,)
+            and A.device == dev and B.device == dev and scale.device == dev and ids.device == dev
+            and w.codes.device == dev
+            and A.is_contiguous() and B.is_contiguous() and scale.is_contiguous() and ids.is_contiguous()):
+        _need(A, "A", bf, (count, r, w.k), dev)
+        _need(B, "B", bf, (count, w.n, r), dev)
+        _need(scale, "scale", torch.float32, (count,), dev)
+        _need(ids, "ids", torch.int32, (m,), dev)
+        _need_weight(w, dev)
     return AdapterSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), count, r), count, r
 
 
@@ -622,8 +635,11 @@ def qlora_linear_fwd_multi(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: to
     bytes of `ws` hold T afterwards."""
     m, dev = X.shape[0], X.device
     out = _out(out, (m, w.n), dev)
-    _need(X, "X", torch.bfloat16, (m, w.k), dev)
-    _need(out, "out", torch.bfloat16, (m, w.n), dev)
+    bf = torch.bfloat16
+    if not (X.dtype is bf and out.dtype is bf and X.shape == (m, w.k) and out.shape == (m, w.n) and out.device == dev
+            and X.is_contiguous() and out.is_contiguous()):
+        _need(X, "X", bf, (m, w.k), dev)
+        _need(out, "out", bf, (m, w.n), dev)
     set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
     ws, ws_bytes = _multi_workspace(QLORA_OP_FWD, m, w.n, w.k, r, count, ws, dev)
     w_c = w.c_struct()
