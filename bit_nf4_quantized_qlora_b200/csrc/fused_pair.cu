@@ -44,6 +44,7 @@
 //            producer waits on) before writing, and arrives on the leader's
 //            wfull barrier; then the epilogue (accumulators -> bf16 tile in
 //            the idle activation ring -> four TMA stores).
+//   warp 19  (many adapters) waits for the projection and takes the tile's list.
 // So after the MMAs of a stage complete, the activation copy and the weight
 // expansion of the stage's next k-step run side by side, not one after the
 // other.

@@ -10,10 +10,11 @@
 // several adapters, so a batch holds the rows of several.
 //
 // The contraction runs over a group's rows, wherever in the batch they are.
-// multi_proj.cu writes each group's row numbers in ascending order into
+// multi_lists.cu writes each group's row numbers in ascending order into
 // slots of 64 (a group starts on a slot of its own); a slot whose rows are
-// consecutive is one TMA box, any other is sixteen row-gathering TMA loads of
-// four rows.  So the work is the rows themselves (plus the last slot's
+// consecutive is one TMA box, any other is up to sixteen row-gathering TMA loads
+// of four rows for each tile, shared out over three warps (one warp issues a load
+// in about 50 cycles).  So the work is the rows themselves (plus the last slot's
 // padding), in every order of the batch, and a group never reads another
 // group's rows.  The pad rows of a group's last slot repeat one of its own rows
 // and are zeroed in R's tile before the product.

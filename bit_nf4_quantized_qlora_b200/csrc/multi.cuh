@@ -14,6 +14,12 @@
 // shared memory for all of the block's steps.  A unit of a K-major adapter
 // matrix is a tile with rows of 128, 64 or 32 bytes under the swizzle of that
 // width, in atoms of 8 rows.
+//
+// The main kernels overlap the projection that makes T or U (multi_proj.cu):
+// they need it only after their main loop.  A unit's product costs about a main
+// k-step's: 128 x 8192 -> 28672 takes 106 us with no adapter, 107 with one of
+// rank 16, 113 with 16 and 123 with 64 (16 steps of four units); 1111 x 11008 ->
+// 4096, r = 64: 116 with none, 118 with one, 135 with 16 in any order.
 #pragma once
 
 #include <type_traits>
@@ -85,18 +91,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
       "r"(smem_u32(bar))
       : "memory");
-}
-
-// 16 bytes of global memory into shared memory, asynchronously (`bytes` = 0:
-// zeros), in the groups that cp_async_commit closes; cp_async_wait<N> leaves
-// the N youngest groups in flight.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // 16 accumulator columns of the warp's 32 lanes.

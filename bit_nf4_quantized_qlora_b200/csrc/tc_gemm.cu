@@ -20,6 +20,7 @@
 //   warp 1      TMEM allocator and single-thread MMA issuer
 //   warps 2..   dequant producers during the main loop (NF4 modes), then the
 //               epilogue: tcgen05.ld -> scale -> bf16 -> global
+//   last warp   (many adapters) waits for the projection, takes the tile's list
 // Stages are guarded by mbarriers: full_a (TMA bytes landed), full_b (dequant
 // warps wrote the B tile), empty (the MMAs reading the stage completed, via
 // tcgen05.commit), acc (all MMAs done).  Every wait is bounded in time: on a
