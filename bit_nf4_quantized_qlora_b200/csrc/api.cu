@@ -271,11 +271,12 @@ int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, cons
   // directly precedes it (unless the caller times the main kernel alone).
   const bool pdl = t_prof_start == nullptr;
   if (e == cudaSuccess) e = prof_mark(t_prof_start, s);
-  if (e == cudaSuccess && dX) e = tc_bwd_dx(dY, m, view(w), U, A, r, dX, s, pdl);      // dX = dY W^ + U A
+  const bool lead = X8 && dX && pdl && m > 128;      // dA beside the input gradient's last wave
+  if (e == cudaSuccess && dX) e = tc_bwd_dx(dY, m, view(w), U, A, r, dX, s, pdl, lead);   // dX = dY W^ + U A
   if (e == cudaSuccess) e = prof_mark(t_prof_stop, s);
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
   if (e == cudaSuccess)
-    e = X8 ? launch_group_grads(nullptr, &x8, U, k, dA, nullptr, nullptr, 0, nullptr, m, r, nullptr, s)
+    e = X8 ? launch_group_grads(nullptr, &x8, U, k, dA, nullptr, nullptr, 0, nullptr, m, r, nullptr, lead, s)
            : tc_tn_skinny(X, m, k, U, r, dA, true, s);                                    // dA = U^T X
   if (e == cudaSuccess && !one_pass) e = tc_tn_skinny(dY, m, n, T ? T : Tw, r, dB, false, s);   // dB = dY^T T
   return cuda_status(e);
@@ -675,7 +676,7 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   if (e == cudaSuccess && dX) e = tc_multi(dY, m, view(w), true, U, ad, lists, dX, s);        // dX = dY W^ + U A_a
   const Act8View x8{X8 ? X8->codes : nullptr, X8 ? X8->scale : nullptr};
   if (e == cudaSuccess)
-    e = launch_group_grads(X, X8 ? &x8 : nullptr, U, k, dA, dY, T ? T : Tw, n, dB, m, a->r, &rows, s);
+    e = launch_group_grads(X, X8 ? &x8 : nullptr, U, k, dA, dY, T ? T : Tw, n, dB, m, a->r, &rows, dX != nullptr, s);
   return cuda_status(e);
 }
 

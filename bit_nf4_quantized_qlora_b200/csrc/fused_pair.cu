@@ -101,6 +101,7 @@ struct __align__(64) PairParams {
   int m, r;
   int num_main, num_lora;
   int pdl;
+  int lead;              // lets the next kernel start beside this one, once U is complete
   Nf4Tables tab;
   MultiParams multi;     // many adapters only
 };
@@ -285,6 +286,12 @@ __global__ void __launch_bounds__(kThreads + (MULTI ? 32 : 0), 1) fused_pair_ker
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
+    // The odd CTAs' warps, which issue nothing, wait for U; the next kernel
+    // starts when every CTA has said so.
+    if (BWD && !MULTI && p.lead) {
+      if (!leader) griddep_wait();
+      griddep_launch();
+    }
     int ok = 1;
     if (leader && lane == 0) {
       for (int it = 0; it < total && ok; ++it) {
@@ -598,9 +605,10 @@ cudaError_t fused_fwd_large(const uint16_t *X, int64_t m, const WeightView &w, c
 }
 
 cudaError_t fused_bwd_dx_large(const uint16_t *dY, int64_t m, const WeightView &w, const uint16_t *U,
-                               const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl) {
+                               const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl, bool lead) {
   const bool lora = U != nullptr && A != nullptr && r > 0;
   PairParams p = common_params(w, m, r, lora, pdl, dX);
+  p.lead = lead ? 1 : 0;
   if (!encode_bf16_map(&p.tmA, dY, m, w.n, 64, 128)) return cudaErrorInvalidValue;
   if (!encode_codes_map(&p.tmCodes, w.codes, w.n, w.k / 2, 32, 64, false)) return cudaErrorInvalidValue;
   if (lora) {

@@ -201,17 +201,17 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     const auto rows_of = [&](int slot) {
       const int64_t i = static_cast<int64_t>(slot) * kSlot + 2 * lane;
       if (slot < 0) return make_int2(-1, -1);
-      if (p.rows.list) return __ldg(reinterpret_cast<const int2 *>(p.rows.list + i));
+      if (p.rows.list) return __ldcg(reinterpret_cast<const int2 *>(p.rows.list + i));
       return make_int2(i < p.rows.m ? static_cast<int>(i) : -1, i + 1 < p.rows.m ? static_cast<int>(i + 1) : -1);
     };
     // Packed only when they are stored: arithmetic here would wait for the loads.
     const auto scales_of = [&](const int2 &row) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       const uint16_t *x = p.scale + static_cast<int64_t>(row.x) * kb + cb, *y = p.scale + static_cast<int64_t>(row.y) * kb + cb;
-      if (row.x >= 0) v.x = __ldg(x);
-      if (row.x >= 0 && cb + 1 < kb) v.y = __ldg(x + 1);
-      if (row.y >= 0) v.z = __ldg(y);
-      if (row.y >= 0 && cb + 1 < kb) v.w = __ldg(y + 1);
+      if (row.x >= 0) v.x = __ldcg(x);
+      if (row.x >= 0 && cb + 1 < kb) v.y = __ldcg(x + 1);
+      if (row.y >= 0) v.z = __ldcg(y);
+      if (row.y >= 0 && cb + 1 < kb) v.w = __ldcg(y + 1);
       return v;
     };
     int slot = walk.next(), slot1 = slot < 0 ? -1 : walk.next(), slot2 = slot1 < 0 ? -1 : walk.next();
@@ -249,7 +249,7 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
     const auto rows_of = [&](int slot) {
       const int r4 = slot * kSlot + 4 * lane;
       if (!p.rows.list || slot < 0 || lane >= 16) return make_int4(r4, r4 + 1, r4 + 2, r4 + 3);
-      return __ldg(reinterpret_cast<const int4 *>(p.rows.list + static_cast<int64_t>(slot) * kSlot) + lane);
+      return __ldcg(reinterpret_cast<const int4 *>(p.rows.list + static_cast<int64_t>(slot) * kSlot) + lane);
     };
     int issued = 0;
     int slot = walk.next(), valid_next = rows_in(slot);
@@ -551,10 +551,13 @@ __global__ void __launch_bounds__(kThreads, 2) group_grads_kernel(const __grid_c
     group_tile<ACT8, true>(p.da, tile);
   else
     group_tile<false, false>(p.db, tile - p.da_tiles);
+  // Started beside the input gradient (see launch): what comes next on the
+  // stream may rely on that one too, so this grid does not end before it.
+  griddep_wait();
 }
 
 template <bool ACT8>
-cudaError_t launch(const GradsParams &p, int tiles, int64_t slots, cudaStream_t stream) {
+cudaError_t launch(const GradsParams &p, int tiles, int64_t slots, bool beside, cudaStream_t stream) {
   static std::atomic<bool> configured[kMaxDevicesPerProcess] = {};
   static ClusterFit fit;
   const void *kernel = reinterpret_cast<const void *>(group_grads_kernel<ACT8>);
@@ -569,13 +572,18 @@ cudaError_t launch(const GradsParams &p, int tiles, int64_t slots, cudaStream_t 
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = static_cast<unsigned>(split);
+  // The input gradient before it lets this grid start once all of its CTAs run
+  // and what both of them read is complete: it takes the SMs that the last wave
+  // leaves idle.
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, group_grads_kernel<ACT8>, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
@@ -608,7 +616,7 @@ bool group_params(GroupParams *p, const uint16_t *L, const Act8View *L8, int64_t
 
 cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint16_t *U, int64_t k, uint16_t *dA,
                                const uint16_t *dY, const uint16_t *T, int64_t n, uint16_t *dB, int64_t m, int32_t r,
-                               const GroupRows *g, cudaStream_t stream) {
+                               const GroupRows *g, bool beside, cudaStream_t stream) {
   GradsParams p{};
   if (!group_params(&p.da, X, X8, m, k, U, r, g, dA)) return cudaErrorInvalidValue;
   if (dB && !group_params(&p.db, dY, nullptr, m, n, T, r, g, dB)) return cudaErrorInvalidValue;
@@ -616,7 +624,7 @@ cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint
   const int tiles = p.da_tiles + (dB ? static_cast<int>((n + 127) / 128) * p.db.rtiles : 0);
   // At most m / 64 slots, and one more for every group with rows.
   const int64_t slots = m / kSlot + (p.da.rows.groups < m ? p.da.rows.groups : m);
-  return X8 ? launch<true>(p, tiles, slots, stream) : launch<false>(p, tiles, slots, stream);
+  return X8 ? launch<true>(p, tiles, slots, beside, stream) : launch<false>(p, tiles, slots, beside, stream);
 }
 
 }  // namespace qlora

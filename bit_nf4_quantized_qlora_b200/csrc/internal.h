@@ -178,11 +178,12 @@ cudaError_t fused_fwd_large(const uint16_t *X, int64_t m, const WeightView &w, c
 
 // The same for m > 128 on CTA pairs (fused_pair.cu).
 cudaError_t fused_bwd_dx_large(const uint16_t *dY, int64_t m, const WeightView &w, const uint16_t *U,
-                               const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl);
+                               const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl, bool lead = false);
 
-// dX = bf16(dY . W^ + U . A); U may be null.
+// dX = bf16(dY . W^ + U . A); U may be null.  `lead` (m > 128): the kernel after
+// it may be launched as its programmatic dependent and then finds U complete.
 cudaError_t tc_bwd_dx(const uint16_t *dY, int64_t m, const WeightView &w, const uint16_t *U,
-                      const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl);
+                      const uint16_t *A, int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl, bool lead = false);
 
 // dX = bf16(dX + D . (U . A) . keep_scale) for U [m x r], A [r x k], k % 64 == 0.
 cudaError_t tc_dropout_add(const uint16_t *U, int64_t m, int32_t r, const uint16_t *A, int64_t k,
@@ -315,10 +316,11 @@ struct Act8View {
 // dA_g = sum over group g's rows i of U[i, :]^T . X[i, :] [r x k], X bf16
 // [m x k] or its checkpoint X8, and (unless dB is null)
 // dB_g = sum of dY[i, :]^T . T[i, :] [n x r]; one group of all rows when g is
-// null.  Every group is written.
+// null.  Every group is written.  `beside`: the kernel before it on the stream
+// lets it start as soon as U, T and the lists are complete.
 cudaError_t launch_group_grads(const uint16_t *X, const Act8View *X8, const uint16_t *U, int64_t k, uint16_t *dA,
                                const uint16_t *dY, const uint16_t *T, int64_t n, uint16_t *dB, int64_t m, int32_t r,
-                               const GroupRows *g, cudaStream_t stream);
+                               const GroupRows *g, bool beside, cudaStream_t stream);
 
 // 8-bit activation checkpoints (act8.cu); numel % 64 == 0.
 cudaError_t launch_act_quantize(const uint16_t *X, int64_t numel, int8_t *codes, uint16_t *scale, cudaStream_t stream);

@@ -153,11 +153,13 @@ __device__ __forceinline__ const int32_t *multi_tile_at(const MultiParams &p, in
 
 // The warp of a kernel that overlaps the projection, for all of its others:
 // waits for the projection (which stops a whole warp, so no warp of the main
-// loop may) and takes the list.  Reads past L1: it was written while this
-// kernel ran.
+// loop may), lets the adapter gradients start, which need the projection but not
+// this kernel's product, and takes the list.  Reads past L1: it was written while
+// this kernel ran.
 template <int QUADS>
 __device__ __forceinline__ void multi_scout(const MultiParams &p, int tile, MultiListSmem<QUADS> &s) {
   griddep_wait();
+  griddep_launch();
   const int32_t *t = multi_tile_at(p, tile);
   const uint4 *mask = reinterpret_cast<const uint4 *>(t + 4 + p.slots);
   const int lane = static_cast<int>(lane_id()), n = __ldcg(t);

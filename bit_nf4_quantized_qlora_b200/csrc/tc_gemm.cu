@@ -757,9 +757,9 @@ cudaError_t tc_fwd(const uint16_t *X, int64_t m, const WeightView &w, const uint
 }
 
 cudaError_t tc_bwd_dx(const uint16_t *dY, int64_t m, const WeightView &w, const uint16_t *U, const uint16_t *A,
-                      int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl) {
+                      int32_t r, uint16_t *dX, cudaStream_t stream, bool pdl, bool lead) {
   // Above 128 rows: the CTA-pair kernel.
-  if (m > 128) return fused_bwd_dx_large(dY, m, w, U, A, r, dX, stream, pdl);
+  if (m > 128) return fused_bwd_dx_large(dY, m, w, U, A, r, dX, stream, pdl, lead);
   TcParams p{};
   const uint32_t bm = 128u;
   const bool lora = U != nullptr && A != nullptr && r > 0;
