@@ -2,8 +2,8 @@
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  PyTorch provides device memory and the current stream; outputs and
-workspaces that the caller does not pass are allocated here with torch (the
-library itself never allocates).  There is no CPU fallback: if the shared
+workspaces that the caller does not pass are allocated here with torch, for the
+stream the call launches on (the library itself never allocates).  There is no CPU fallback: if the shared
 library is missing or a call fails, a ``QLoRAError`` is raised.
 """
 import ctypes
@@ -186,6 +186,20 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """What a call allocates, from the pool of the stream it launches on.  A
+    block of the current stream's pool would go back to it as soon as the call
+    drops the tensor, and could still be in use there when the call starts."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)        # 0 and 1 name the default stream
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need_cuda(*ts: Optional[torch.Tensor]) -> None:
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -270,9 +284,8 @@ def qlora_quantize_4bit_dq(W: torch.Tensor, codebook: int, absmax_fp32: Optional
     n_scales = max(n_groups(numel), 1) + (1 if dq_format == QLORA_DQ_FP8_MEAN else 0)
     if out is None:
         dev = W.device
-        out = NF4Weight(torch.empty(numel // 2, dtype=torch.uint8, device=dev),
-                        torch.empty(numel // BLOCK, dtype=torch.uint8, device=dev),
-                        torch.empty(n_scales, dtype=torch.float32, device=dev), n, k, codebook, dq_format)
+        out = NF4Weight(_empty(numel // 2, torch.uint8, dev, stream), _empty(numel // BLOCK, torch.uint8, dev, stream),
+                        _empty(n_scales, torch.float32, dev, stream), n, k, codebook, dq_format)
     else:
         if out.group_scale.numel() < n_scales:
             raise ValueError(f"out.group_scale holds {out.group_scale.numel()} entries, {n_scales} needed")
@@ -288,7 +301,7 @@ def qlora_quantize_4bit_dq(W: torch.Tensor, codebook: int, absmax_fp32: Optional
 def qlora_dequant(w: NF4Weight, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """NF4Weight -> bf16 W^ [n x k]."""
     if out is None:
-        out = torch.empty(w.n, w.k, dtype=torch.bfloat16, device=w.codes.device)
+        out = _empty((w.n, w.k), torch.bfloat16, w.codes.device, stream)
     _need_cuda(out)
     ws = w.c_struct()
     _check("qlora_dequant", lib().qlora_dequant(ctypes.byref(ws), out.data_ptr(), _stream(stream)))
@@ -302,9 +315,9 @@ def qlora_merge_adapter(w: NF4Weight, A: Optional[torch.Tensor], B: Optional[tor
     A, B, r = _lora_args(A, B, r)
     dev = w.codes.device
     if out_bf16 is None and want_bf16:
-        out_bf16 = torch.empty(w.n, w.k, dtype=torch.bfloat16, device=dev)
+        out_bf16 = _empty((w.n, w.k), torch.bfloat16, dev, stream)
     if out_f32 is None and want_f32:
-        out_f32 = torch.empty(w.n, w.k, dtype=torch.float32, device=dev)
+        out_f32 = _empty((w.n, w.k), torch.float32, dev, stream)
     _need_cuda(A, B, out_bf16, out_f32)
     ws = w.c_struct()
     _check("qlora_merge_adapter",
@@ -319,10 +332,10 @@ def _lora_args(A, B, r):
     return A, B, r
 
 
-def _workspace(op, m, n, k, r, ws, device):
+def _workspace(op, m, n, k, r, ws, device, stream):
     need = qlora_workspace_bytes(op, m, n, k, r)
     if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty(need, torch.uint8, device, stream)
     return ws, (ws.numel() * ws.element_size() if ws is not None else 0)
 
 
@@ -335,8 +348,8 @@ def qlora_linear_fwd(X: torch.Tensor, w: NF4Weight, A: Optional[torch.Tensor] = 
     _need_cuda(X, A, B, out, ws)
     m = X.shape[0]
     if out is None:
-        out = torch.empty(m, w.n, dtype=torch.bfloat16, device=X.device)
-    ws, ws_bytes = _workspace(QLORA_OP_FWD, m, w.n, w.k, r, ws, X.device)
+        out = _empty((m, w.n), torch.bfloat16, X.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_FWD, m, w.n, w.k, r, ws, X.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_fwd",
            lib().qlora_linear_fwd(X.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
@@ -353,8 +366,8 @@ def qlora_linear_bwd_dx(dY: torch.Tensor, w: NF4Weight, A: Optional[torch.Tensor
     _need_cuda(dY, A, B, out, ws)
     m = dY.shape[0]
     if out is None:
-        out = torch.empty(m, w.k, dtype=torch.bfloat16, device=dY.device)
-    ws, ws_bytes = _workspace(QLORA_OP_BWD_DX, m, w.n, w.k, r, ws, dY.device)
+        out = _empty((m, w.k), torch.bfloat16, dY.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_BWD_DX, m, w.n, w.k, r, ws, dY.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_bwd_dx",
            lib().qlora_linear_bwd_dx(dY.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
@@ -370,10 +383,10 @@ def qlora_lora_bwd(X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor, B: torch.
     m, k = X.shape
     n = dY.shape[1]
     if dA is None:
-        dA = torch.empty(r, k, dtype=torch.bfloat16, device=X.device)
+        dA = _empty((r, k), torch.bfloat16, X.device, stream)
     if dB is None:
-        dB = torch.empty(n, r, dtype=torch.bfloat16, device=X.device)
-    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, X.device)
+        dB = _empty((n, r), torch.bfloat16, X.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, X.device, stream)
     _check("qlora_lora_bwd",
            lib().qlora_lora_bwd(X.data_ptr(), dY.data_ptr(), m, n, k, A.data_ptr(), B.data_ptr(), r, float(scale),
                                 dA.data_ptr(), dB.data_ptr(), _ptr(ws), ws_bytes, _stream(stream)))
@@ -390,12 +403,12 @@ def qlora_linear_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch.T
     m, k = X.shape
     n = dY.shape[1]
     if dX is None and want_dx:
-        dX = torch.empty(m, k, dtype=torch.bfloat16, device=X.device)
+        dX = _empty((m, k), torch.bfloat16, X.device, stream)
     if dA is None:
-        dA = torch.empty(r, k, dtype=torch.bfloat16, device=X.device)
+        dA = _empty((r, k), torch.bfloat16, X.device, stream)
     if dB is None:
-        dB = torch.empty(n, r, dtype=torch.bfloat16, device=X.device)
-    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, X.device)
+        dB = _empty((n, r), torch.bfloat16, X.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, X.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_bwd",
            lib().qlora_linear_bwd(dY.data_ptr(), X.data_ptr(), _ptr(T), m, ctypes.byref(ws_c), A.data_ptr(),
@@ -411,7 +424,7 @@ def qlora_lora_dropout(X: torch.Tensor, p: float, seed: int, offset: int, out: O
     _need_cuda(X, out)
     m, k = X.shape
     if out is None:
-        out = torch.empty_like(X)
+        out = _empty(X.shape, X.dtype, X.device, stream)
     _check("qlora_lora_dropout", lib().qlora_lora_dropout(X.data_ptr(), m, k, float(p), int(seed), int(offset),
                                                           out.data_ptr(), _stream(stream)))
     return out
@@ -425,10 +438,10 @@ def qlora_linear_fwd_dropout(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: 
     _need_cuda(X, A, B, out, Xd, ws)
     m = X.shape[0]
     if out is None:
-        out = torch.empty(m, w.n, dtype=torch.bfloat16, device=X.device)
+        out = _empty((m, w.n), torch.bfloat16, X.device, stream)
     if Xd is None:
-        Xd = torch.empty_like(X)
-    ws, ws_bytes = _workspace(QLORA_OP_FWD, m, w.n, w.k, r, ws, X.device)
+        Xd = _empty(X.shape, X.dtype, X.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_FWD, m, w.n, w.k, r, ws, X.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_fwd_dropout",
            lib().qlora_linear_fwd_dropout(X.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
@@ -444,8 +457,8 @@ def qlora_linear_bwd_dx_dropout(dY: torch.Tensor, w: NF4Weight, A: torch.Tensor,
     _need_cuda(dY, A, B, out, ws)
     m = dY.shape[0]
     if out is None:
-        out = torch.empty(m, w.k, dtype=torch.bfloat16, device=dY.device)
-    ws, ws_bytes = _workspace(QLORA_OP_BWD_DX, m, w.n, w.k, r, ws, dY.device)
+        out = _empty((m, w.k), torch.bfloat16, dY.device, stream)
+    ws, ws_bytes = _workspace(QLORA_OP_BWD_DX, m, w.n, w.k, r, ws, dY.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_bwd_dx_dropout",
            lib().qlora_linear_bwd_dx_dropout(dY.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
@@ -464,7 +477,7 @@ def qlora_linear_fwd_noalloc(X: torch.Tensor, w: NF4Weight, A: Optional[torch.Te
     _need_cuda(X, A, B, out)
     m = X.shape[0]
     if out is None:
-        out = torch.empty(m, w.n, dtype=torch.bfloat16, device=X.device)
+        out = _empty((m, w.n), torch.bfloat16, X.device, stream)
     ws_c = w.c_struct()
     _check("qlora_linear_fwd_noalloc",
            lib().qlora_linear_fwd_noalloc(X.data_ptr(), m, ctypes.byref(ws_c), _ptr(A), _ptr(B), r, float(scale),
@@ -481,9 +494,9 @@ class Act8:
     k: int
 
     @classmethod
-    def empty(cls, m: int, k: int, device) -> "Act8":
-        return cls(torch.empty(m, k, dtype=torch.int8, device=device),
-                   torch.empty(m, k // BLOCK, dtype=torch.bfloat16, device=device), m, k)
+    def empty(cls, m: int, k: int, device, stream=None) -> "Act8":
+        return cls(_empty((m, k), torch.int8, device, stream), _empty((m, k // BLOCK), torch.bfloat16, device, stream),
+                   m, k)
 
     def c_struct(self) -> Act8C:
         return Act8C(self.codes.data_ptr(), self.scale.data_ptr(), self.m, self.k)
@@ -521,8 +534,8 @@ def _need_weight(w: NF4Weight, device) -> None:
         raise ValueError(f"the weight is on {w.codes.device}, not on {device}")
 
 
-def _out(t: Optional[torch.Tensor], shape, device) -> torch.Tensor:
-    return torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t
+def _out(t: Optional[torch.Tensor], shape, device, stream) -> torch.Tensor:
+    return _empty(shape, torch.bfloat16, device, stream) if t is None else t
 
 
 def _need_ws(ws: Optional[torch.Tensor], device) -> None:
@@ -550,7 +563,7 @@ def qlora_act_quantize(X: torch.Tensor, out: Optional[Act8] = None, stream=None)
     if X.dtype is not torch.bfloat16 or not X.is_contiguous():
         _need(X, "X", torch.bfloat16, (m, k), dev)
     if out is None:
-        out = Act8.empty(m, k, dev)
+        out = Act8.empty(m, k, dev, stream)
     _need_act8(out, m, k, dev)
     _check("qlora_act_quantize", lib().qlora_act_quantize(X.data_ptr(), m, k, out.codes.data_ptr(),
                                                           out.scale.data_ptr(), _stream_on(dev, stream)))
@@ -561,7 +574,7 @@ def qlora_act_dequant(act: Act8, out: Optional[torch.Tensor] = None, stream=None
     """The checkpoint's X^ = bf16(codes . scale) [m x k]."""
     dev = act.codes.device
     _need_act8(act, act.m, act.k, dev)
-    out = _out(out, (act.m, act.k), dev)
+    out = _out(out, (act.m, act.k), dev, stream)
     _need(out, "out", torch.bfloat16, (act.m, act.k), dev)
     a = act.c_struct()
     _check("qlora_act_dequant", lib().qlora_act_dequant(ctypes.byref(a), out.data_ptr(), _stream_on(dev, stream)))
@@ -576,14 +589,14 @@ def qlora_linear_bwd_act8(dY: torch.Tensor, act: Act8, w: NF4Weight, A: torch.Te
     checkpoint; T = the forward's bf16(s X A^T) [m x r]."""
     m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
     if dX is not None or want_dx:
-        dX = _out(dX, (m, k), dev)
-    dA, dB = _out(dA, (r, k), dev), _out(dB, (n, r), dev)
+        dX = _out(dX, (m, k), dev, stream)
+    dA, dB = _out(dA, (r, k), dev, stream), _out(dB, (n, r), dev, stream)
     for t, name, shape in ((dY, "dY", (m, n)), (A, "A", (r, k)), (B, "B", (n, r)), (T, "T", (m, r)),
                            (dX, "dX", (m, k)), (dA, "dA", (r, k)), (dB, "dB", (n, r))):
         _need(t, name, bf, shape, dev)
     _need_act8(act, m, k, dev)
     _need_weight(w, dev)
-    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, dev)
+    ws, ws_bytes = _workspace(QLORA_OP_LORA_BWD, m, n, k, r, ws, dev, stream)
     _need_ws(ws, dev)
     w_c, a_c = w.c_struct(), act.c_struct()
     _check("qlora_linear_bwd_act8",
@@ -617,11 +630,11 @@ def _adapter_set(A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, ids: tor
     return AdapterSetC(A.data_ptr(), B.data_ptr(), scale.data_ptr(), count, r), count, r
 
 
-def _multi_workspace(op, m, n, k, r, count, ws, device):
+def _multi_workspace(op, m, n, k, r, count, ws, device, stream):
     if ws is None:
         need = qlora_multi_workspace_bytes(op, m, n, k, r, count)
         # Sizes the library refuses have no workspace; the call reports them.
-        ws = torch.empty(need if need < 1 << 62 else 0, dtype=torch.uint8, device=device)
+        ws = _empty(need if need < 1 << 62 else 0, torch.uint8, device, stream)
     _need_ws(ws, device)
     return ws, ws.numel() * ws.element_size()
 
@@ -634,14 +647,14 @@ def qlora_linear_fwd_multi(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: to
     B [count x n x r], scale fp32 [count], ids int32 [m].  The first m*r*2
     bytes of `ws` hold T afterwards."""
     m, dev = X.shape[0], X.device
-    out = _out(out, (m, w.n), dev)
+    out = _out(out, (m, w.n), dev, stream)
     bf = torch.bfloat16
     if not (X.dtype is bf and out.dtype is bf and X.shape == (m, w.k) and out.shape == (m, w.n) and out.device == dev
             and X.is_contiguous() and out.is_contiguous()):
         _need(X, "X", bf, (m, w.k), dev)
         _need(out, "out", bf, (m, w.n), dev)
     set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
-    ws, ws_bytes = _multi_workspace(QLORA_OP_FWD, m, w.n, w.k, r, count, ws, dev)
+    ws, ws_bytes = _multi_workspace(QLORA_OP_FWD, m, w.n, w.k, r, count, ws, dev, stream)
     w_c = w.c_struct()
     _check("qlora_linear_fwd_multi",
            lib().qlora_linear_fwd_multi(X.data_ptr(), m, ctypes.byref(w_c), ctypes.byref(set_c), ids.data_ptr(),
@@ -659,8 +672,8 @@ def qlora_linear_bwd_multi(dY: torch.Tensor, X, w: NF4Weight, A: torch.Tensor, B
     m, n, k, dev, bf = dY.shape[0], w.n, w.k, dY.device, torch.bfloat16
     set_c, count, r = _adapter_set(A, B, scale, ids, m, w, dev)
     if dX is not None or want_dx:
-        dX = _out(dX, (m, k), dev)
-    dA, dB = _out(dA, (count, r, k), dev), _out(dB, (count, n, r), dev)
+        dX = _out(dX, (m, k), dev, stream)
+    dA, dB = _out(dA, (count, r, k), dev, stream), _out(dB, (count, n, r), dev, stream)
     act = X if isinstance(X, Act8) else None
     if act is not None:
         _need_act8(act, m, k, dev)
@@ -668,7 +681,7 @@ def qlora_linear_bwd_multi(dY: torch.Tensor, X, w: NF4Weight, A: torch.Tensor, B
     for t, name, shape in ((dY, "dY", (m, n)), (X, "X", (m, k)), (T, "T", (m, r)), (dX, "dX", (m, k)),
                            (dA, "dA", (count, r, k)), (dB, "dB", (count, n, r))):
         _need(t, name, bf, shape, dev)
-    ws, ws_bytes = _multi_workspace(QLORA_OP_LORA_BWD, m, n, k, r, count, ws, dev)
+    ws, ws_bytes = _multi_workspace(QLORA_OP_LORA_BWD, m, n, k, r, count, ws, dev, stream)
     w_c = w.c_struct()
     a_c = ctypes.byref(act.c_struct()) if act is not None else None
     _check("qlora_linear_bwd_multi",
