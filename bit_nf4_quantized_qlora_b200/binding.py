@@ -398,7 +398,8 @@ def qlora_linear_bwd(dY: torch.Tensor, X: torch.Tensor, w: NF4Weight, A: torch.T
                      dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None, want_dx: bool = True,
                      ws: Optional[torch.Tensor] = None, stream=None):
     """(dX or None, dA, dB) of the layer in one call; T = the forward's
-    bf16(s X A^T) (the first m*r*2 bytes of its workspace) or None."""
+    bf16(s X A^T) (the first m*r*2 bytes of its workspace, which may be `ws`)
+    or None."""
     _need_cuda(dY, X, A, B, T, dX, dA, dB, ws)
     m, k = X.shape
     n = dY.shape[1]

@@ -220,6 +220,28 @@ int launch_fwd(const uint16_t *X, const uint16_t *Xa, int64_t m, const qlora_nf4
 
 namespace {
 
+// The two [m x r] parts at the start of a backward's workspace, `part` bytes
+// each: one for U, the other for a T that the call computes.  A T of the caller's
+// may be in either (the forward leaves its own at the start of its workspace);
+// U takes the other.  False if T lies elsewhere in the `need` bytes the call
+// writes.
+struct BackwardParts {
+  uint16_t *U, *T;
+};
+bool place_parts(const uint16_t *T, int64_t m, int32_t r, void *ws, size_t part, size_t need, BackwardParts *out) {
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  uint16_t *first = static_cast<uint16_t *>(ws), *second = reinterpret_cast<uint16_t *>(base + part);
+  *out = BackwardParts{first, second};
+  const uintptr_t w = reinterpret_cast<uintptr_t>(ws), lo = reinterpret_cast<uintptr_t>(T);
+  const uintptr_t hi = lo + static_cast<uintptr_t>(m) * static_cast<uintptr_t>(r) * 2u;
+  if (T == nullptr || hi <= w || lo >= w + need) return true;
+  if (lo >= w && hi <= w + part) {
+    *out = BackwardParts{second, first};
+    return true;
+  }
+  return lo >= w + part && hi <= w + 2 * part;
+}
+
 // The whole backward of one adapter, X given as bf16 or as its checkpoint X8.
 int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, const uint16_t *T, int64_t m,
                const qlora_nf4_weight *w, const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX,
@@ -231,6 +253,8 @@ int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, cons
   if (m < 0 || m > (int64_t(1) << 31)) return QLORA_ERR_SHAPE;
   if (!aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB)) return QLORA_ERR_ALIGN;
   if ((dX && !aligned16(dX)) || (T && !aligned16(T))) return QLORA_ERR_ALIGN;
+  const size_t mr = m > 0 ? round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u) : 0;
+  BackwardParts parts{};
   if (m > 0) {
     if ((!X && !X8) || !dY) return QLORA_ERR_NULL;
     if (!aligned16(X) || !aligned16(dY)) return QLORA_ERR_ALIGN;
@@ -241,6 +265,7 @@ int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, cons
     const size_t need = qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, w->n, w->k, r);
     if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+    if (!place_parts(T, m, r, ws, mr, need, &parts)) return QLORA_ERR_WORKSPACE;
   }
   st = check_device();
   if (st != QLORA_OK) return st;
@@ -252,9 +277,7 @@ int linear_bwd(const uint16_t *dY, const uint16_t *X, const qlora_act8 *X8, cons
     if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, static_cast<size_t>(n) * static_cast<size_t>(r) * 2u, s);
     return cuda_status(e);
   }
-  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
-  uint16_t *U = static_cast<uint16_t *>(ws);
-  uint16_t *Tw = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + mr);
+  uint16_t *U = parts.U, *Tw = parts.T;
   void *scratch = static_cast<uint8_t *>(ws) + 2 * mr;
   const size_t scratch_bytes = ws_bytes - 2 * mr;
   // U once, for the input gradient and for dA; T from the forward when given.
@@ -640,6 +663,8 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   if (!dA || !dB) return QLORA_ERR_NULL;
   if (!aligned16(dA) || !aligned16(dB) || (dX && !aligned16(dX)) || (T && !aligned16(T))) return QLORA_ERR_ALIGN;
   const int64_t n = w->n, k = w->k;
+  const size_t mr = m > 0 ? round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u) : 0;
+  BackwardParts parts{};
   if (m > 0) {
     // X from exactly one of the two; a checkpoint needs the forward's T.
     if (!dY || (!X && !X8) || (X && X8) || (X8 && !T)) return QLORA_ERR_NULL;
@@ -651,6 +676,7 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
     const size_t need = qlora_multi_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, a->r, a->count);
     if (ws == nullptr || ws_bytes < need) return QLORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+    if (!place_parts(T, m, a->r, ws, mr, need, &parts)) return QLORA_ERR_WORKSPACE;
   }
   st = check_device();
   if (st != QLORA_OK) return st;
@@ -663,9 +689,8 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
     return cuda_status(e);
   }
   const AdapterView ad{a->A, a->B, a->scale, ids, a->count, a->r};
-  const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(a->r) * 2u);
   uint8_t *p = static_cast<uint8_t *>(ws);
-  uint16_t *U = reinterpret_cast<uint16_t *>(p), *Tw = reinterpret_cast<uint16_t *>(p + mr);
+  uint16_t *U = parts.U, *Tw = parts.T;
   const int64_t steps = (n + 63) / 64;
   const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, steps));
   const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), m, a->count);

@@ -260,6 +260,9 @@ int qlora_lora_bwd(const uint16_t *X, const uint16_t *dY, int64_t m, int64_t n, 
  *   T  = bf16(s . X . A^T): pass the forward's (qlora_linear_fwd leaves it at
  *        the start of its workspace, [m x r] row-major), or NULL to compute it
  *        here.  With dropout, X is the forward's Xd and T its workspace.
+ *        One workspace may serve both passes: T may stay at the start of ws
+ *        (or fill the next m*r*2 bytes, rounded up to 256, behind it); a T that
+ *        lies elsewhere in the bytes this call needs gives QLORA_ERR_WORKSPACE.
  *   dY, X  in   bf16 [m x n], [m x k];  A, B as in the forward, r > 0
  *   dX, dA, dB out  (dX may be NULL); ws >= qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, r)
  * m == 0 writes zeros to dA and dB.  Same results as qlora_linear_bwd_dx
@@ -331,7 +334,8 @@ int qlora_act_dequant(const qlora_act8 *x, uint16_t *X, qlora_stream_t stream);
 
 /* qlora_linear_bwd with X read from a checkpoint of it (with dropout: of Xd):
  *   dX, dB  as qlora_linear_bwd;   dA = bf16(U^T . X^)
- * T is required (the forward's: it saw X itself).  x8->m == m and x8->k == w->k,
+ * T is required (the forward's: it saw X itself) and may lie in ws as in
+ * qlora_linear_bwd.  x8->m == m and x8->k == w->k,
  * else QLORA_ERR_SHAPE.  ws >= qlora_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, r).
  * m == 0 writes zeros to dA and dB and reads neither x8 nor T.               */
 int qlora_linear_bwd_act8(const uint16_t *dY, const qlora_act8 *x8, const uint16_t *T, int64_t m,
@@ -386,7 +390,8 @@ int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight 
  *   dB_a  = bf16( sum over a's rows of dY[i]^T . T[i] ) [count x n x r]
  * X is given as bf16 (x8 NULL) or as its checkpoint (X NULL; X^ takes its
  * place): exactly one of the two, else QLORA_ERR_NULL.  T is the forward's, or
- * NULL to compute it here from X (not from a checkpoint).  dA and dB are
+ * NULL to compute it here from X (not from a checkpoint); it may lie in ws as
+ * in qlora_linear_bwd.  dA and dB are
  * overwritten for every adapter; one without rows gets zeros.
  *   ws >= qlora_multi_workspace_bytes(QLORA_OP_LORA_BWD, m, n, k, r, count)
  * m == 0 writes zeros to dA and dB.                                          */
