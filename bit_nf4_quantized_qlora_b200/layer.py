@@ -180,6 +180,8 @@ class MultiQLoRALinear(torch.nn.Module):
     def forward(self, x: torch.Tensor, ids: torch.Tensor, act: Optional[B.Act8] = None) -> torch.Tensor:
         lead = x.shape[:-1]
         X = x.reshape(-1, x.shape[-1]).contiguous()
+        if ids is None:
+            raise ValueError("a layer of many adapters needs the rows' ids")
         if ids.shape != lead[:ids.dim()]:
             raise ValueError(f"ids of shape {list(ids.shape)} do not lead rows of shape {list(lead)}")
         rows = ids.reshape(ids.shape + (1,) * (len(lead) - ids.dim())).expand(lead).reshape(-1).contiguous()
@@ -207,7 +209,8 @@ class DecoderLayer(torch.nn.Module):
     (q, k, v, o; causal, no positional rotation) and a SwiGLU MLP
     (gate, up, down).  The RMSNorm gains are 1 (frozen).
 
-    With projections of many adapters, ``forward(x, ids)`` passes them the ids.
+    With projections of many adapters, all or some of the seven,
+    ``forward(x, ids)`` passes those the ids.
     With `act8` the projections keep their inputs in 8 bits, one checkpoint for
     q, k and v and one for gate and up.  o keeps its bf16 input, which
     attention's own backward holds in any case."""
@@ -219,11 +222,11 @@ class DecoderLayer(torch.nn.Module):
         self.lin = torch.nn.ModuleDict(linears)
 
     def _project(self, names: Sequence[str], x: torch.Tensor, ids: Optional[torch.Tensor], act8: bool):
-        args = (x,) if ids is None else (x, ids)
+        kw = {}
         if act8 and torch.is_grad_enabled():
-            act = B.qlora_act_quantize(x.detach().reshape(-1, x.shape[-1]).contiguous())
-            return [self.lin[name](*args, act=act) for name in names]
-        return [self.lin[name](*args) for name in names]
+            kw["act"] = B.qlora_act_quantize(x.detach().reshape(-1, x.shape[-1]).contiguous())
+        lins = [self.lin[name] for name in names]
+        return [lin(x, ids, **kw) if isinstance(lin, MultiQLoRALinear) else lin(x, **kw) for lin in lins]
 
     def forward(self, x: torch.Tensor, ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         b, t, h = x.shape
