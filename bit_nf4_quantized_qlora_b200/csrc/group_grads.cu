@@ -17,7 +17,8 @@
 // in about 50 cycles).  So the work is the rows themselves (plus the last slot's
 // padding), in every order of the batch, and a group never reads another
 // group's rows.  The pad rows of a group's last slot repeat one of its own rows
-// and are zeroed in R's tile before the product.
+// and are zeroed in both tiles before the product (in one alone, an infinity of
+// the repeated row would meet a zero).
 //
 // A CTA takes 128 columns of L, 64 columns of R and an equal share of the
 // slots, whatever groups they belong to: a cluster of up to 8 CTAs covers all
@@ -358,15 +359,20 @@ __device__ __forceinline__ void group_tile(const GroupParams &p, int tile) {
       if (stop < part.e) {
         ok = ok && ready();
         if (ok) {
-          // Zero rows of R: whole 128-byte rows, so the swizzle inside them
-          // does not matter.
-          const int valid = part.rows % kSlot;
-          const uint32_t r_s = base + static_cast<uint32_t>(s) * kStageBytes + kLBytes;
+          // Zero rows of L's two slabs and of R, as far as the product reads:
+          // whole 128-byte rows, so the swizzle inside them does not matter.
+          const int valid = part.rows % kSlot, chunks = (valid + 15) / 16;
+          const uint32_t l_s = base + static_cast<uint32_t>(s) * kStageBytes;
           const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-          for (int c = valid * 8 + lane; c < kSlot * 8; c += 32) sts128(r_s + static_cast<uint32_t>(c) * 16u, zero);
+          for (int c = valid * 8 + lane; c < chunks * 128; c += 32) {
+            const uint32_t at = l_s + static_cast<uint32_t>(c) * 16u;
+            sts128(at, zero);
+            sts128(at + kLBytes / 2u, zero);
+            sts128(at + kLBytes, zero);
+          }
           fence_proxy_async_smem();
           __syncwarp();
-          multiply(acc, stop == part.b, (valid + 15) / 16);
+          multiply(acc, stop == part.b, chunks);
           advance();
         }
       }
