@@ -74,6 +74,7 @@ static_assert(kSmemBytes <= 227u * 1024u, "shared memory");
 struct __align__(64) StreamParams {
   CUtensorMap tmCodes;           // codes [n x k/2] bytes, box {128, tile rows}, 128B swizzle
   CUtensorMap tmQ;               // absmax codes [n x k/64] bytes, box {16, tile rows} (MODE 2)
+  const uint8_t *codes;          // [n x k/2] (OFFSET kernels)
   const uint8_t *absmax_q;       // [n x k/64]
   const float *group_scale;      // [ceil(n k / 16384)] (+ the tensor mean, E4M3 + mean format)
   const float *mu;               // E4M3 + mean format: the tensor mean; else null
@@ -86,7 +87,8 @@ struct __align__(64) StreamParams {
   int64_t n, k;
   int adapters;
   float unscale;                 // takes the levels' common factor out of the block constants
-  uint32_t minus_offset;         // minus the levels' offset, a bf16 pair (OFFSET kernels)
+  float offset;                  // the levels' offset (OFFSET kernels)
+  uint32_t minus_offset;         // minus that, a bf16 pair
   int m, r;
   int ntiles;                    // ceil(n / tile rows)
   int chunks;                    // ceil((k / 64) / 4)
@@ -169,6 +171,35 @@ __device__ __forceinline__ void word_mma(float (&d)[4], uint32_t w_g, uint32_t w
 template <class F, int... S>
 __device__ __forceinline__ bool slot_pass(const F &f, uint32_t ph, std::integer_sequence<int, S...>) {
   return f(ph, std::integral_constant<int, S>{}...);
+}
+
+// Row n's sum with token mi where the block sums came out non-finite: what the
+// token's infinities and NaN make of it by the weights' own values.  With an
+// offset an infinity also meets the opposite infinity of the offset's product,
+// and the block sum is NaN whatever the weight.  `sum` if all activations are
+// finite.
+template <bool FP8>
+__device__ __noinline__ float non_finite_sum(const StreamParams &p, int64_t n, int mi, float sum) {
+  const uint16_t *x = p.X + static_cast<int64_t>(mi) * p.k;
+  const float mu = load_mu(p.mu);
+  float acc = 0.f;
+  bool any = false;
+  for (int64_t i = 0; i < p.k; i += 8) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + i));
+    const uint32_t xx[4] = {v.x, v.y, v.z, v.w};
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t bits = (xx[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+      if ((bits & 0x7F80u) != 0x7F80u) continue;
+      const int64_t at = n * p.k + i + e, block = at >> 6;
+      const uint32_t byte = __ldg(p.codes + (at >> 1)), code = e & 1 ? byte & 15u : byte >> 4;
+      const float c = block_constant(__ldg(p.absmax_q + block), group_constant(__ldg(p.group_scale + (block >> 8)), FP8),
+                                     FP8, mu);
+      const uint32_t w = pack_bf16x2((p.tab.level[code] - p.offset) * c, 0.f);
+      acc = fmaf(__uint_as_float(bits << 16), bf16lo_to_f32(w), acc);
+      any = true;
+    }
+  }
+  return any ? acc : sum;
 }
 
 // FP8: the absmax codes are E4M3 offsets from the tensor mean (p.mu).
@@ -463,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_stream_kernel(const __grid_c
 #pragma unroll
     for (uint32_t peer = 0; peer < kMaxCluster; ++peer)
       if (peer < csize) sum += part[peer];
+    if (OFFSET && !isfinite(sum)) sum = non_finite_sum<FP8>(p, n, mi, sum);
     // The token's adapter; an id outside the set means none.
     const int ad = p.ids ? __ldg(p.ids + mi) : 0;
     if (p.r > 0 && (!p.ids || (ad >= 0 && ad < p.adapters))) {
@@ -560,6 +592,8 @@ cudaError_t launch_gemv_stream(const uint16_t *X, int64_t m, const uint8_t *code
   p.ids = ids;
   p.adapters = adapters;
   p.unscale = unscale;
+  p.codes = codes;
+  p.offset = offset;
   p.minus_offset = bf16_pair(-offset);
   p.Y = Y;
   p.err = device_error_word();
