@@ -608,9 +608,10 @@ int qlora_act_dequant(const qlora_act8 *x, uint16_t *X, qlora_stream_t stream) {
 }
 
 size_t qlora_multi_workspace_bytes(int op, int64_t m, int64_t n, int64_t k, int32_t r, int32_t count) {
-  if (m < 0 || m > QLORA_MULTI_MAX_ROWS || n <= 0 || k <= 0 || r <= 0 || count <= 0 ||
-      count > QLORA_MULTI_MAX_ADAPTERS)
+  const int64_t most = int64_t(1) << 31;
+  if (m < 0 || m > QLORA_MULTI_MAX_ROWS || n <= 0 || n > most || (n % 8) != 0 || k <= 0 || k > most || (k % 64) != 0)
     return SIZE_MAX;
+  if (r <= 0 || r > 256 || (r % 16) != 0 || count <= 0 || count > QLORA_MULTI_MAX_ADAPTERS) return SIZE_MAX;
   const size_t mr = round_up(static_cast<size_t>(m) * static_cast<size_t>(r) * 2u);
   const size_t lists = m > 0 ? round_up(tile_lists_bytes(m, count)) + round_up(group_rows_bytes(m, count)) : 0;
   switch (op) {

@@ -160,6 +160,11 @@ class MultiQLoRALinear(torch.nn.Module):
 
     def __init__(self, w: B.NF4Weight, A: torch.Tensor, Bm: torch.Tensor, scale: torch.Tensor, act8: bool = False):
         super().__init__()
+        if A.dim() != 3 or A.shape[2] != w.k or Bm.shape != (A.shape[0], w.n, A.shape[1]) or scale.shape != A.shape[:1]:
+            raise ValueError(f"A, B and scale of shape {list(A.shape)}, {list(Bm.shape)} and {list(scale.shape)} are no "
+                             f"adapters of a [{w.n} x {w.k}] weight")
+        if not 0 < A.shape[1] <= 256 or A.shape[1] % 16:
+            raise ValueError(f"the adapters' rank must be a multiple of 16 up to 256, not {A.shape[1]}")
         self.w = w
         self.act8 = act8
         self.A = torch.nn.Parameter(A.to(torch.bfloat16).contiguous())
@@ -171,7 +176,10 @@ class MultiQLoRALinear(torch.nn.Module):
                       act8: bool = False) -> "MultiQLoRALinear":
         """Adapters (A [r_a x k], B [n x r_a], alpha_a) of any ranks up to 256,
         padded with zeros to the largest (a multiple of 16)."""
-        r = max(16, -(-max(A.shape[0] for A, _, _ in adapters) // 16) * 16)
+        ranks = [A.shape[0] for A, _, _ in adapters]
+        if not ranks or not 0 < min(ranks) <= max(ranks) <= 256:
+            raise ValueError(f"one or more adapters of ranks 1 to 256 are needed, not {ranks}")
+        r = -(-max(ranks) // 16) * 16
         As = torch.stack([F.pad(A.to(torch.bfloat16), (0, 0, 0, r - A.shape[0])) for A, _, _ in adapters])
         Bs = torch.stack([F.pad(Bm.to(torch.bfloat16), (0, r - Bm.shape[1])) for _, Bm, _ in adapters])
         scale = torch.tensor([alpha / A.shape[0] for A, _, alpha in adapters], dtype=torch.float32, device=As.device)
