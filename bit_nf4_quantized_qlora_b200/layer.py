@@ -171,6 +171,14 @@ class MultiQLoRALinear(torch.nn.Module):
         self.B = torch.nn.Parameter(Bm.to(torch.bfloat16).contiguous())
         self.register_buffer("scale", scale.to(torch.float32).contiguous())
 
+    def _apply(self, fn, recurse=True):
+        # The scales are fp32 in a model of any type; they only change device.
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
+
     @classmethod
     def from_adapters(cls, w: B.NF4Weight, adapters: Sequence[Tuple[torch.Tensor, torch.Tensor, float]],
                       act8: bool = False) -> "MultiQLoRALinear":
