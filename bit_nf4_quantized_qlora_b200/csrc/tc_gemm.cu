@@ -657,6 +657,13 @@ cudaError_t launch(const TcParams &p, int grid_n, int grid_m, cudaStream_t strea
 
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+int device_sms() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 using CfgFwd1 = Cfg<256, 1, false, true, false, false>;
 using CfgFwd1S = Cfg<256, 1, false, true, false, false, true>;
 using CfgBwd1 = Cfg<256, 1, false, true, true, false>;
@@ -678,10 +685,7 @@ using CfgBwd1SM = Cfg<256, 1, false, true, true, false, true, kEpiStore, true>;
 // products, which fit two to an SM; one for the input gradient), at least two
 // k-steps per CTA, at most 8 CTAs per cluster.
 int choose_split(int64_t tiles, int ksteps, int per_sm) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int64_t sp = (static_cast<int64_t>(per_sm) * sms) / (tiles > 0 ? tiles : 1);
+  int64_t sp = (static_cast<int64_t>(per_sm) * device_sms()) / (tiles > 0 ? tiles : 1);
   if (sp > 8) sp = 8;
   if (sp > ksteps / 2) sp = ksteps / 2;
   return sp < 1 ? 1 : static_cast<int>(sp);
@@ -802,8 +806,8 @@ int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps) {
   if (m <= 128) return 128;
   const int64_t gn = (cols + 255) / 256, gm = (m + 127) / 128;
   const int64_t pair_ctas = 2 * gn * ((m + 511) / 512);
-  const int64_t tiles = gn * gm;
-  if (pair_ctas > 74 || tiles > 148) return 512;
+  const int64_t tiles = gn * gm, sms = device_sms();
+  if (pair_ctas > sms / 2 || tiles > sms) return 512;
   const int sp = choose_split(tiles, static_cast<int>(ksteps), 1);
   return 85 * (ksteps + sp - 1) / sp < 55 * ksteps ? 128 : 512;
 }
