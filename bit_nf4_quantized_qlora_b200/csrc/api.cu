@@ -646,7 +646,7 @@ int qlora_linear_fwd_multi(const uint16_t *X, int64_t m, const qlora_nf4_weight 
     const int64_t steps = w->k / 64;
     uint8_t *p = static_cast<uint8_t *>(ws) + mr;
     const TileLists lists = carve_tile_lists(p, m, a->count, multi_tile_rows(m, w->n, steps));
-    const GroupRows rows = carve_group_rows(p + round_up(tile_lists_bytes(m, a->count)), m, a->count);
+    const GroupRows rows = carve_group_rows(p + round_up(tile_lists_bytes(m, a->count)), a->count);
     e = launch_multi_lists(ad, m, lists, rows, T, nullptr, s);
     if (e == cudaSuccess)
       e = launch_multi_proj(X, m, w->k, ad, false, T, rows, multi_grid(m, w->n, steps, lists.rows), s);
@@ -694,7 +694,7 @@ int qlora_linear_bwd_multi(const uint16_t *dY, const uint16_t *X, const qlora_ac
   uint16_t *U = parts.U, *Tw = parts.T;
   const int64_t steps = (n + 63) / 64;
   const TileLists lists = carve_tile_lists(p + 2 * mr, m, a->count, multi_tile_rows(m, k, steps));
-  const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), m, a->count);
+  const GroupRows rows = carve_group_rows(p + 2 * mr + round_up(tile_lists_bytes(m, a->count)), a->count);
   cudaError_t e = launch_multi_lists(ad, m, lists, rows, U, T ? nullptr : Tw, s);
   if (e == cudaSuccess && !T) e = launch_multi_proj(X, m, k, ad, false, Tw, rows, MultiGrid{}, s);   // T = s_a X A_a^T
   if (e == cudaSuccess)                                                                       // U = s_a dY B_a

@@ -276,7 +276,7 @@ struct GroupRows {
   int32_t *start, *count, *list;
   int32_t groups;
 };
-GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups);
+GroupRows carve_group_rows(void *scratch, int32_t groups);
 size_t group_rows_bytes(int64_t m, int32_t groups);
 
 // Fills both kinds of lists, and with zeros the rows without an adapter of up

@@ -121,12 +121,12 @@ __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.
 struct MultiParams {
   const int32_t *lists;
   int64_t stride;
-  int32_t slots, rows;
+  int32_t slots;
   int32_t r, width;
   const uint16_t *A, *B;    // [count x r x k], [count x n x r]
 };
 inline MultiParams multi_params(const AdapterView &ad, const TileLists &l) {
-  return MultiParams{l.base, l.stride, l.slots, l.rows, ad.r, unit_width(ad.r), ad.A, ad.B};
+  return MultiParams{l.base, l.stride, l.slots, ad.r, unit_width(ad.r), ad.A, ad.B};
 }
 
 // One tile's list: its first entries (adapter ids and the masks of QUADS * 128

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) multi_lists_kernel(const ListParams 
 
 }  // namespace
 
-GroupRows carve_group_rows(void *scratch, int64_t m, int32_t groups) {
+GroupRows carve_group_rows(void *scratch, int32_t groups) {
   GroupRows g{};
   int32_t *base = static_cast<int32_t *>(scratch);
   g.groups = groups;
