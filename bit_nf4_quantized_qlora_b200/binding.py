@@ -646,7 +646,8 @@ def qlora_linear_fwd_multi(X: torch.Tensor, w: NF4Weight, A: torch.Tensor, B: to
     """Y[i] = bf16(X[i] . W^T + bf16(s_a X[i] A_a^T) . B_a^T), a = ids[i]; an
     id outside [0, count) means no adapter.  X bf16 [m x k], A [count x r x k],
     B [count x n x r], scale fp32 [count], ids int32 [m].  The first m*r*2
-    bytes of `ws` hold T afterwards."""
+    bytes of `ws` hold T afterwards, which qlora_linear_bwd_multi takes (it may
+    have the same `ws`)."""
     m, dev = X.shape[0], X.device
     out = _out(out, (m, w.n), dev, stream)
     bf = torch.bfloat16
