@@ -21,8 +21,9 @@
 // one, so rint gives the definition's code, ties included.
 //
 // Both kernels are bound by HBM: 2 B read and 1.03 B written per element
-// (save), the reverse for the restore.  X [8192 x 11008]: 45 and 43 us, 6.1 and
-// 6.3 TB/s (0.92 and 0.97 of a copy).  Wider pieces in the save (16 elements a thread, so that
+// (save), the reverse for the restore.  X [8192 x 11008], a second of them on
+// end: 49 and 43 us, 5.6 and 6.3 TB/s (0.85 and 0.97 of a copy); the first ones
+// take 44 and 43.  Wider pieces in the save (16 elements a thread, so that
 // codes leave in 16-byte stores: 45 us against 52 with 8) and narrower ones in
 // the restore (one 16-byte store a piece: 43 us against 49 .. 58 with two)
 // keep every warp's stores in whole consecutive lines.

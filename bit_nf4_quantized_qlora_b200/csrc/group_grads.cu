@@ -36,10 +36,11 @@
 //
 // Checkpoint form: L's tile arrives as 64 x 128 codes (half the bytes); the
 // eight epilogue warps expand it to the bf16 tile the product reads, half a
-// block of 64 elements (one scale) per thread: two integer and half a packed
-// floating-point instruction per element.  dA of 11008 x 64 from 4096 rows: 32 us,
-// 1.5 TB/s of codes; a slot is a chain of about 1300 cycles in the expand warps
-// (two groups of four warps in turn, with two bf16 tiles, took the same time).
+// block of 64 elements (one scale) per thread: one and a half integer and one
+// packed floating-point instruction per element.  dA of 11008 x 64 from 4096
+// rows: 33 us, 1.45 TB/s of codes, scales, U and dA; a CTA takes about 2700
+// cycles a slot with two CTAs on the SM, a chain through the expand warps (two
+// groups of four warps in turn, with two bf16 tiles, took the same time).
 #include <cuda.h>
 
 #include "act8.cuh"

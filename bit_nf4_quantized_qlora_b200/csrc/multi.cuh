@@ -16,10 +16,12 @@
 // width, in atoms of 8 rows.
 //
 // The main kernels overlap the projection that makes T or U (multi_proj.cu):
-// they need it only after their main loop.  A unit's product costs about a main
-// k-step's: 128 x 8192 -> 28672 takes 106 us with no adapter, 107 with one of
-// rank 16, 113 with 16 and 123 with 64 (16 steps of four units); 1111 x 11008 ->
-// 4096, r = 64: 116 with none, 118 with one, 135 with 16 in any order.
+// they need it only after their main loop.  Back to back, 128 x 8192 -> 28672
+// takes 106 us with no adapter in the batch, 108 with one of rank 16, 113 with
+// 16 and 126 with 64: 16 steps of four 16-column units, 1.25 us each, where a
+// main k-step takes 0.8.  1111 x 11008 -> 4096, r = 64, in any order: 135 with
+// none, 140 with one, 152 with 16 and 201 with 64, the projection of that many
+// adapters included (a main k-step of a 512-row tile takes 0.75).
 #pragma once
 
 #include <type_traits>
@@ -104,9 +106,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 }
 
 // One lane of a converged warp, the same at every call.  Copies and products
-// are issued under it: their operands live in warp-wide registers, and under a
-// test of the lane's number the compiler moves each of them through a loop over
-// the lanes (a masked product took 600 cycles to issue, 100 under this).
+// are issued under it: a masked product took 600 cycles to issue under a test
+// of the lane's number and 100 under this.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -115,7 +116,6 @@ __device__ __forceinline__ bool elect_lane() {
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 
 // A call's tile lists and adapters, as kernel parameters.
 struct MultiParams {

@@ -370,8 +370,8 @@ int qlora_linear_bwd_act8(const uint16_t *dY, const qlora_act8 *x8, const uint16
  * Time and workspace grow with `count` too, used or not: for m > 16 and in the
  * backward each adapter of the set costs one pass over the ids, and the backward
  * writes the zeros of every absent one.  4096 rows of 8 adapters through 4096 ->
- * 4096, r = 16: forward 120 us with 8 in the set, 147 with 1000 and 282 with
- * 10000; backward 137 and 416 with 1000.
+ * 4096, r = 16: forward 132 us with 8 in the set, 147 with 1000 and 275 with
+ * 10000; backward 151 and 410 with 1000.
  *
  * There are no forms with LoRA dropout, without a workspace or with profiling
  * events (qlora_linear_fwd_dropout, qlora_linear_fwd_noalloc,
