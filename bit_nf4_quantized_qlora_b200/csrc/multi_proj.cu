@@ -46,8 +46,8 @@ constexpr uint32_t kColBytes = kBK * 2u;          // shared memory of one rank c
 constexpr uint32_t kTmemCols = 256;               // r <= 256
 // One CTA to an SM, or two with half the ring each for ranks up to 64, where a
 // half still holds three stages (backward of 2000 x 4096, r = 16, 32 adapters:
-// 100 us with two and 103 with one; of 4096 x 11008, r = 128, 8 adapters: 448
-// with two of two stages and 426 with one of four).
+// 93 us with two and 96 with one; of 4096 x 11008, r = 128, 8 adapters: 403
+// with two of two stages and 400 with one of four).
 constexpr uint32_t kRing = 200u * 1024u;
 constexpr int kSharedRank = 64;
 constexpr int stages_of(int r, int per_sm) {
@@ -359,10 +359,10 @@ cudaError_t launch(ProjParams &p, int64_t slots, int64_t free_sms, int64_t main_
   // The projection keeps to the SMs that the product launched on its heels
   // leaves free, if it is done there before that product needs it: 64 columns
   // of a slot take about 0.33 us, a k-step of the product 0.55 to 0.85 us.
-  // Forward of 1111 x 11008 -> 4096, r = 64: 123 us beside the product and 139
-  // in front of it with 6 adapters, 193 and 191 with 64 (where the estimate is
-  // the product's whole main loop); 128 x 8192 -> 28672, r = 16, 64 adapters: 123
-  // and 137.  One CTA to an SM then, since CTAs that could share one are spread
+  // Forward of 1111 x 11008 -> 4096, r = 64: 136 us beside the product and 150
+  // in front of it with 6 adapters, 205 and 207 with 64 (where the estimate is
+  // the product's whole main loop); 128 x 8192 -> 28672, r = 16, 64 adapters: 126
+  // and 142.  One CTA to an SM then, since CTAs that could share one are spread
   // over them all.
   // K is split over the largest clusters of which one per slot fits at once.
   const bool beside = free_sms >= 16 && slots * p.nk <= 2 * free_sms * main_steps;

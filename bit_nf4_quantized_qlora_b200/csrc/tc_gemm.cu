@@ -799,9 +799,9 @@ cudaError_t tc_bwd_dx(const uint16_t *dY, int64_t m, const WeightView &w, const 
 // 512-row tiles on CTA pairs do a k-step in about 0.55 us, 128-row tiles in
 // about 0.85 us but split the k-steps over up to 8 CTAs: those are the faster
 // ones while the pairs cover less than half of the SMs.  4 adapters, r = 16:
-// backward of 300 x 11008 (k = 4096) 111 us on 128-row tiles and 129 on pairs,
-// forward of 300 x 4096 (n = 1024) 29 and 51; on more SMs the two meet (600 rows
-// of 4096 x 4096, backward: 64 and 65).
+// backward of 300 x 11008 (k = 4096) 102 us on 128-row tiles and 126 on pairs,
+// forward of 300 x 4096 (n = 1024) 29 and 52; on more SMs the two meet (600 rows
+// of 4096 x 4096, backward: 65 and 65).
 int multi_tile_rows(int64_t m, int64_t cols, int64_t ksteps) {
   if (m <= 128) return 128;
   const int64_t gn = (cols + 255) / 256, gm = (m + 127) / 128;
