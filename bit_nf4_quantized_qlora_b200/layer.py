@@ -187,6 +187,10 @@ class MultiQLoRALinear(torch.nn.Module):
         ranks = [A.shape[0] for A, _, _ in adapters]
         if not ranks or not 0 < min(ranks) <= max(ranks) <= 256:
             raise ValueError(f"one or more adapters of ranks 1 to 256 are needed, not {ranks}")
+        for i, (A, Bm, _) in enumerate(adapters):
+            if A.shape[1:] != (w.k,) or Bm.shape != (w.n, A.shape[0]):
+                raise ValueError(f"adapter {i} of shapes {list(A.shape)} and {list(Bm.shape)} does not fit a "
+                                 f"[{w.n} x {w.k}] weight")
         r = -(-max(ranks) // 16) * 16
         As = torch.stack([F.pad(A.to(torch.bfloat16), (0, 0, 0, r - A.shape[0])) for A, _, _ in adapters])
         Bs = torch.stack([F.pad(Bm.to(torch.bfloat16), (0, r - Bm.shape[1])) for _, Bm, _ in adapters])

@@ -42,3 +42,13 @@ def test_modules_refuse_ranks_no_call_takes():
                      (torch.zeros(16, 64), torch.zeros(24, 16), torch.ones(1))):
         with pytest.raises(ValueError, match="shape"):
             L.MultiQLoRALinear(w, A, Bm, s)
+
+
+def test_an_adapter_whose_halves_do_not_fit_is_refused():
+    """Padding would hide columns of B that no row of A feeds."""
+    w = B.NF4Weight(None, None, None, 24, 64)
+    ok = (torch.ones(8, 64), torch.ones(24, 8), 16.0)
+    for bad in ((torch.ones(8, 64), torch.ones(24, 16), 16.0), (torch.ones(16, 64), torch.ones(24, 8), 16.0),
+                (torch.ones(8, 128), torch.ones(24, 8), 16.0), (torch.ones(8, 64), torch.ones(32, 8), 16.0)):
+        with pytest.raises(ValueError, match="adapter 1"):
+            L.MultiQLoRALinear.from_adapters(w, [ok, bad])
