@@ -8,6 +8,12 @@
 // quantized base is served with the adapter, and one base serves several;
 // "QLoRA and Quantized Training", In code: r and alpha.
 //
+// The sums are fp32; T and U are rounded to bf16 once, because the products that
+// take them are bf16 tensor-core products (with A_a, B_a, X and dY) and the
+// one-adapter layer rounds them there too.  Where the adapter term is of the base
+// product's size dX and dA are then off by up to 0.0024 (rms, relative), for 0.0017
+// of their own rounding alone; two bf16 parts would double the adapter steps.
+//
 // tcgen05 path (multi_proj_kernel).  A CTA takes a slot of up to 64 rows of one
 // adapter, wherever in the batch they lie: one TMA box per k-step when they are
 // consecutive, row-gathering loads of four rows otherwise, and only as many as
